@@ -168,6 +168,24 @@ class MultipoleIndex:
         L.check(self.lib.mp_cluster_build(ctypes.byref(self.h), _ptr(K), _ptr(V), int(n), _ptr(init_centroids),
                                           _stream(stream)), "mp_cluster_build")
 
+    def build_paged(self, cache, table, lens, n, stream=None):
+        """Cluster the first n tokens of the paged cache's requests from scratch.
+
+        cache: a PagedCache of this index's heads, head_dim and dtype; table,
+        lens: its block table and lengths, one request per sequence of the batch
+        (a request shorter than n contributes zero rows).  Gathers the pages
+        (mp_paged_gather) and builds (mp_cluster_build).
+        """
+        c = self.cfg
+        if (cache.kv_heads, cache.head_dim, cache.torch_dtype) != (c.kv_heads, c.head_dim, c.torch_dtype):
+            raise ValueError(f"the index holds {c.kv_heads} heads of {c.head_dim} {c.torch_dtype}")
+        if table.shape[0] != c.batch or cache.device != self.device:
+            raise ValueError(f"the index holds {c.batch} sequences on {self.device}")
+        if not 0 <= n <= c.max_tokens:
+            L.check(L.MP_ENOSPC if n > 0 else L.MP_EINVAL, "build_paged")
+        K, V = cache.gather(table, lens, n, stream=stream)
+        self.build(K, V, stream=stream)
+
     def update(self, K_new, V_new, stream=None):
         """Append generated tokens; returns True when blocks were re-clustered (mp_cluster_update)."""
         n = K_new.shape[2]

@@ -12,9 +12,10 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libmpattn.so")
-SOURCES = ["api.cu", "assign_tc.cu", "decode.cu", "decode_static.cu", "decode_unit.cu", "kmeans.cu"]
+SOURCES = ["api.cu", "assign_tc.cu", "decode.cu", "decode_static.cu", "decode_unit.cu", "kmeans.cu", "paged.cu",
+           "paged_attend.cu"]
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
-              "-Xcompiler", "-fPIC", "--shared"]
+              "-Xcompiler", "-fPIC", "--shared", "--threads", "0"]
 
 
 def nvcc():

@@ -18,7 +18,7 @@
  *      d  = head_dim (64 or 128).
  *  - `stream` is a cudaStream_t passed as void* (NULL = legacy default
  *    stream).  All device work is enqueued on it; no call synchronises the
- *    host except mp_check_device_error.
+ *    host except mp_check_device_error and mp_paged_check_error.
  *  - The library never allocates device memory.  The caller allocates the
  *    index workspace and the decode scratch (sizes from mp_workspace_size)
  *    and owns every buffer.  Inputs passed to a call must stay alive until the
@@ -52,7 +52,7 @@ typedef enum {
   MP_EDEVICE = 5         /* the device error word was set (see mp_check_device_error) */
 } mp_status;
 
-typedef enum { MP_F32 = 0, MP_BF16 = 1 } mp_dtype;
+typedef enum { MP_F32 = 0, MP_BF16 = 1, MP_F16 = 2 /* paged cache only */ } mp_dtype;
 
 /* Initial centroids of a from-scratch build. */
 typedef enum {
@@ -277,6 +277,139 @@ mp_status mp_dense_decode(const mp_config* cfg, const void* K, const void* V, in
  * phase_events[0] at the start and phase_events[i] at the end of phase i.
  * A static string; "" for a NULL index. */
 const char* mp_decode_phases(const mp_index* idx);
+
+/* ---------------------------------------------------------------------------
+ * Paged cache: the keys and values of many requests of different lengths, in
+ * pages of a common pool, before (or without) clustering.  The pages describe
+ * one cache of one length; these calls hold the cache a server has, attend a
+ * prompt's chunks and single tokens over it, and copy requests out in the
+ * layout that mp_cluster_build and mp_dense_decode take.
+ *
+ * A request's token at position p lies in page table[b][p / page_tokens], row
+ * p % page_tokens; the slot of a token is page * page_tokens + row.  A step of
+ * a batch has new_tokens[b] new rows for request b, its rows consecutive and
+ * the requests in order: row cu[b] + i of request b is its token at position
+ * lens[b] - (cu[b+1] - cu[b]) + i, lens[b] counting the new tokens.  Lengths,
+ * offsets and tables are device memory and never read by the host, so that a
+ * captured step can be replayed with other lengths.  Like all entry points
+ * these validate what the host can see, launch on `stream`, do not synchronise
+ * and allocate nothing.  A data-dependent fault sets a bit of the cache's
+ * error word and skips the access: 1 a page, slot, length or offset outside its
+ * range, 4 a bounded wait gave up, 8 a step that does not fit (mp_paged_plan)
+ * or a request with more rows than max_new (mp_paged_attend).
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int32_t kv_heads, head_dim;        /* head_dim 64 or 128 */
+  int32_t num_pages, page_tokens;    /* page_tokens a power of two, 16 to 256 */
+  int32_t dtype;                     /* MP_F32, MP_BF16 or MP_F16 */
+  int32_t reserved;                  /* must be 0 */
+  /* Elements between pages, heads and tokens of K and of V (16-byte multiples;
+   * all 0: [num_pages, kv_heads, page_tokens, head_dim], contiguous).  Any order
+   * of the three axes, and K and V interleaved in one buffer, are possible. */
+  int64_t page_stride, head_stride, token_stride;
+} mp_paged_config;
+
+/* Host-side handle of a paged cache over caller-owned K and V.  Plain data;
+ * read-only for callers. */
+typedef struct {
+  mp_paged_config cfg;               /* strides filled in */
+  void* K;
+  void* V;
+  int32_t* err;                      /* the cache's error word (device) */
+  int32_t device;
+  int32_t reserved;
+  uint64_t maps[64];                 /* tensor maps (private) */
+} mp_paged_cache;
+
+typedef struct {
+  int32_t batch;                     /* requests, at most 8192 */
+  int32_t table_pages;               /* pages a request may hold: columns of the table */
+  int32_t table_stride;              /* elements between the table's rows */
+  int32_t rows;                      /* rows of slots and positions */
+  int32_t free_capacity;             /* elements of free_pages */
+  int32_t reserved;                  /* must be 0 */
+  const int32_t* lens;               /* [batch] tokens cached so far */
+  const int32_t* new_tokens;         /* [batch] tokens that arrive */
+  int32_t* table;                    /* [batch, table_pages] in and out */
+  const int32_t* free_pages;         /* [free_capacity] ids of free pages, a stack */
+  const int32_t* free_count;         /* [1] how many of them are valid */
+  int32_t* lens_out;                 /* [batch], may be lens */
+  int32_t* cu_out;                   /* [batch + 1] */
+  int64_t* slots_out;                /* [rows] */
+  int32_t* positions_out;            /* [rows] */
+  int32_t* free_count_out;           /* [1], may be free_count */
+} mp_paged_plan_args;
+
+typedef struct {
+  int32_t batch;                     /* requests, at most 65535 */
+  int32_t q_heads;                   /* kv_heads * (1, 2, 4 or 8) */
+  int32_t rows;                      /* rows of Q and O */
+  int32_t max_new;                   /* most rows that one request has; 0: rows */
+  int32_t table_pages, table_stride; /* as in mp_paged_plan_args */
+  const int32_t* table;
+  const int32_t* lens;               /* [batch] tokens cached, the new ones among them */
+  const int32_t* cu;                 /* [batch + 1] first row of each request */
+  const void* Q;                     /* [rows, q_heads, head_dim] */
+  void* O;
+  int64_t q_row_stride, q_head_stride, o_row_stride, o_head_stride;  /* elements, 16-byte multiples */
+  float scale;                       /* 0: 1 / sqrt(head_dim) */
+  float softcap;                     /* 0: none; else z = softcap * tanh(z / softcap) */
+  int32_t window;                    /* 0: none; else a row sees the last `window` positions up to its own */
+  uint32_t flags;                    /* MP_ATTEND_FULL */
+  const float* slopes;               /* [q_heads] or NULL: z -= slopes[h] * |position - key|, after the cap */
+  const int32_t* prefix;             /* [batch] or NULL: every row also sees the keys before prefix[b] */
+  const int32_t* first_key;          /* [rows] or NULL: a row sees no key before first_key[row] */
+  float* lse;                        /* [rows, q_heads] or NULL: log of the sum of exp(z); -inf for an empty row */
+} mp_paged_attend_args;
+
+#define MP_ATTEND_FULL 1u /* rows see the keys after their own position too */
+
+/* A handle over K and V (device, 16-byte aligned) with the error word `d_err`
+ * (device, 4 bytes, zero).  Records the current device.  MP_EUNSUPPORTED for
+ * other head dims or page sizes. */
+mp_status mp_paged_init(const mp_paged_config* cfg, void* K, void* V, int32_t* d_err, mp_paged_cache* out);
+
+/* The addresses of a step: for every request the pages that its new tokens
+ * need are taken from the end of free_pages (requests in order, a request's
+ * pages in order) and written to its row of the table; lens_out = lens +
+ * new_tokens; cu_out = the new tokens' exclusive sums and their total; for
+ * each of the total rows its slot and its position; slot -1 and position 0 for
+ * the rows behind; free_count_out = what is left.  Held table entries are not
+ * written, so the same inputs give the same outputs again.  All or nothing:
+ * when a length is negative, the pages or the rows do not suffice or a request
+ * would need more than table_pages, bit 8 is set, the table, the lengths and
+ * the count stay as they are, cu_out is 0 and every slot is -1. */
+mp_status mp_paged_plan(const mp_paged_cache* cache, const mp_paged_plan_args* args, void* stream);
+
+/* Write rows of K_new, V_new ([rows, kv_heads, head_dim], strides in elements,
+ * 16-byte multiples, the same for both) to their slots (device int64 [rows]).
+ * A negative slot is skipped.  Of rows with the same slot, each 16 bytes come
+ * from one of them. */
+mp_status mp_paged_append(const mp_paged_cache* cache, const void* K_new, const void* V_new, int64_t row_stride,
+                          int64_t head_stride, const int64_t* slots, int32_t rows, void* stream);
+
+/* Attention of the step's rows over their requests' cached keys.  Row r at
+ * position p (above) sees the keys j in [lo, hi), hi = max(p + 1, min(prefix,
+ * len)) or len with MP_ATTEND_FULL, lo = max(first_key, p - window + 1);
+ * z_j = scale q.k_j, capped, biased; O = sum e^z v / sum e^z over the keys it
+ * sees, whatever other keys hold; 0 for a row that sees none.  Rows from
+ * cu[batch] on are left as they were.  Accumulation and softmax are fp32.
+ * `d_scratch` (256-byte aligned, mp_paged_attend_scratch bytes, contents
+ * irrelevant) holds the partial results of one call at a time. */
+mp_status mp_paged_attend(const mp_paged_cache* cache, const mp_paged_attend_args* args, void* d_scratch,
+                          size_t scratch_bytes, void* stream);
+mp_status mp_paged_attend_scratch(const mp_paged_cache* cache, const mp_paged_attend_args* args, size_t* bytes);
+
+/* Copy the tokens [0, n) of every request into K_out, V_out, contiguous
+ * [batch, kv_heads, n, head_dim]: what mp_cluster_build takes.  Rows from
+ * lens[b] on are zero.  n <= table_pages * page_tokens. */
+mp_status mp_paged_gather(const mp_paged_cache* cache, int32_t batch, const int32_t* table, int32_t table_pages,
+                          int32_t table_stride, const int32_t* lens, int32_t n, void* K_out, void* V_out,
+                          void* stream);
+
+/* mp_check_device_error for a paged cache: synchronises `stream`, reads and
+ * clears the error word. */
+mp_status mp_paged_check_error(const mp_paged_cache* cache, int32_t* code, void* stream);
 
 /* Static description of a status code. */
 const char* mp_status_str(mp_status s);
