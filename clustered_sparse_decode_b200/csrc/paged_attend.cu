@@ -1,8 +1,8 @@
-// Attention of new tokens over a paged cache: the choice of kernel, and the
-// row-by-row kernel.
+// Attention of new tokens over a paged cache: the choice of kernel, its scratch,
+// and the row-by-row kernel.
 #include <algorithm>
 
-#include "paged_common.cuh"
+#include "paged_work.cuh"
 
 namespace mp {
 namespace paged {
@@ -32,7 +32,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_plain(const Attend a) {
   RowState<T, D> s;
   attend_row<T, D>(a, lo, r, i, hq, 0, r.len, s);
   T* o = reinterpret_cast<T*>(a.O + (int64_t)t * a.o_row_b + (int64_t)hq * a.o_head_b) + lane * (D / 32);
-  const bool none = s.m == -INFINITY;
+  const bool none = s.l == 0.f;
   const float inv = none ? 0.f : 1.f / s.l;
 #pragma unroll
   for (int e = 0; e < D / 32; ++e) o[e] = from_f32<T>(s.acc[e] * inv);
@@ -91,18 +91,89 @@ static void launch_plain(const Attend& a, int D, cudaStream_t st) {
   else rows_plain<T, 64><<<grid, kRowWarps * 32, 0, st>>>(a);
 }
 
+// How a call is done.  Few (token, head) rows a KV head: paged_rows.cu, blocks
+// in clusters of one unit (one launch) while a block's part of the longest
+// request that the table can hold stays short, shares over all SMs otherwise
+// (three launches, the same time whatever the lengths).
+constexpr int kFewCells = 32;          // rows that the few-rows kernel takes
+constexpr int kFewParts = 2 * 148;     // two blocks an SM
+constexpr int kClusterBlocks = 16;     // blocks of keys of a clustered block at most
+
+struct Way {
+  bool few;
+  int cells, cluster, entries, rows, parts;
+};
+
+static Way way_of(const mp_paged_cache& c, const mp_paged_attend_args& p) {
+  Way w{};
+  const int G = p.q_heads / c.cfg.kv_heads, max_new = p.max_new ? p.max_new : p.rows;
+  if (c.cfg.dtype == MP_F32 || (int64_t)max_new * G > kFewCells) return w;
+  w.few = true;
+  w.cells = max_new * G;
+  const int64_t units = (int64_t)p.batch * c.cfg.kv_heads;
+  const int64_t blocks = ((int64_t)p.table_pages * c.cfg.page_tokens + kFewBlock - 1) / kFewBlock;
+  int k = 1;
+  while (k < 8 && units * k < kFewParts) k *= 2;
+  if (blocks <= (int64_t)kClusterBlocks * k && units * k <= (1 << 30)) {
+    w.cluster = k;
+    return w;
+  }
+  w.entries = p.rows / max_new + p.batch;
+  w.rows = few_rows(w.cells);
+  w.parts = kFewParts;
+  return w;
+}
+
+static size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// The scratch of a split call: count, sums, entries, partial results.
+static size_t lay_work(const Way& w, int D, void* base, Work* out) {
+  if (w.entries == 0) return 0;
+  size_t at = 256;
+  const size_t before = at;
+  at = align256(at + (size_t)(w.entries + 1) * sizeof(int64_t));
+  const size_t entry = at;
+  at = align256(at + (size_t)w.entries * sizeof(Entry));
+  const size_t part = at;
+  at = align256(at + (size_t)2 * w.parts * w.rows * (2 + D) * sizeof(float));
+  if (out) {
+    char* s = static_cast<char*>(base);
+    out->count = reinterpret_cast<int32_t*>(s);
+    out->before = reinterpret_cast<int64_t*>(s + before);
+    out->entry = reinterpret_cast<Entry*>(s + entry);
+    out->part = reinterpret_cast<float*>(s + part);
+    out->parts = w.parts;
+  }
+  return at;
+}
+
 }  // namespace paged
 
-size_t paged_attend_scratch_bytes(const mp_paged_cache&, const mp_paged_attend_args&) { return 0; }
+size_t paged_attend_scratch_bytes(const mp_paged_cache& c, const mp_paged_attend_args& p) {
+  if (p.batch == 0 || p.rows == 0) return 0;
+  return paged::lay_work(paged::way_of(c, p), c.cfg.head_dim, nullptr, nullptr);
+}
 
-mp_status paged_attend_impl(const mp_paged_cache& c, const mp_paged_attend_args& p, void*, size_t, cudaStream_t st) {
+mp_status paged_attend_impl(const mp_paged_cache& c, const mp_paged_attend_args& p, void* scratch, size_t,
+                            cudaStream_t st) {
   const paged::Attend a = paged::args_of(c, p);
-  switch (c.cfg.dtype) {
-    case MP_F32: paged::launch_plain<float>(a, c.cfg.head_dim, st); break;
-    case MP_BF16: paged::launch_plain<__nv_bfloat16>(a, c.cfg.head_dim, st); break;
-    default: paged::launch_plain<__half>(a, c.cfg.head_dim, st);
+  const paged::Way w = paged::way_of(c, p);
+  cudaError_t e = cudaSuccess;
+  if (w.few) {
+    paged::Work work{};
+    paged::lay_work(w, c.cfg.head_dim, scratch, &work);
+    work.least = 4;
+    e = paged::attend_few(a, c, work, w.cells, w.cluster, st);
+  } else if (c.cfg.dtype == MP_F32) {
+    paged::launch_plain<float>(a, c.cfg.head_dim, st);
+  } else if (c.cfg.dtype == MP_BF16) {
+    paged::launch_plain<__nv_bfloat16>(a, c.cfg.head_dim, st);
+  } else {
+    paged::launch_plain<__half>(a, c.cfg.head_dim, st);
   }
-  return cudaGetLastError() == cudaSuccess ? MP_OK : MP_ECUDA;
+  if (e == cudaSuccess) return cudaGetLastError() == cudaSuccess ? MP_OK : MP_ECUDA;
+  cudaGetLastError();
+  return MP_ECUDA;
 }
 
 }  // namespace mp

@@ -136,6 +136,7 @@ __device__ void attend_row(const Attend& a, int b, const Request& r, int i, int 
     for (int e = 0; e < E; ++e) s.acc[e] = s.acc[e] * keep + w * to_f32(vr[e]);
     s.m = m;
   }
+  if (s.l != s.l) s.m = s.l;         // a NaN among the keys seen must not pass for "nothing seen"
 }
 
 }  // namespace paged

@@ -1,0 +1,68 @@
+// The work list of a split attention call and its share-out.
+//
+// An entry is a tile of one request's rows; its cost is the number of key
+// blocks that its rows can see.  With H heads, the units (entry, head) laid
+// end to end, blocks inside, are one line of W blocks, of which part c of N
+// gets [c W / N, (c + 1) W / N): equal shares whatever the requests' lengths,
+// most units whole.  A unit cut between parts leaves a partial result in each
+// (two at most a part: the unit its share begins inside of, and the one it
+// ends inside of), and a second kernel joins them in the parts' order, so the
+// result does not depend on timing.
+#pragma once
+
+#include "paged_common.cuh"
+
+namespace mp {
+namespace paged {
+
+struct Entry {
+  int32_t b, tile, k0, n;            // request, tile of its rows, first key (a block's), blocks
+};
+
+struct Work {
+  int32_t* count;                    // [1] entries
+  int64_t* before;                   // [entries + 1] blocks of the entries before, for one head
+  Entry* entry;                      // [entries]
+  float* part;                       // [2 parts][rows (2 + D)]: maxima, sums, numerators
+  int32_t parts;                     // parts launched
+  int32_t least;                     // blocks a part gets at least, as far as there are that many
+};
+
+__device__ __forceinline__ int64_t share(int64_t W, int N, int c) { return W * c / N; }
+// parts in use: as many as launched, fewer when shares would be smaller than `least`
+__device__ __forceinline__ int parts_used(const Work& w, int64_t W) {
+  const int64_t n = (W + w.least - 1) / w.least;
+  return (int)(n < w.parts ? (n < 1 ? 1 : n) : w.parts);
+}
+// the part that block x of the line belongs to
+__device__ __forceinline__ int part_of(int64_t W, int N, int64_t x) {
+  int c = (int)(x * N / W);
+  while (c + 1 < N && share(W, N, c + 1) <= x) ++c;
+  while (c > 0 && share(W, N, c) > x) --c;
+  return c;
+}
+// the entry that block x of the line belongs to
+__device__ __forceinline__ int entry_of(const Work& w, int E, int H, int64_t x) {
+  int lo = 0, hi = E;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (w.before[mid] * H <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// Makes the list: tiles of `tile` rows (tokens), blocks of `block` keys.
+cudaError_t launch_work(const Attend& a, const Work& w, int tile, int block, cudaStream_t st);
+// Joins the partial results of cut units: `rows` (token, head) rows a unit, G heads a token.
+cudaError_t launch_join(const Attend& a, const Work& w, int dtype, int D, int tile, int rows, int max_entries,
+                        cudaStream_t st);
+
+// Few rows (paged_rows.cu): `cells` (token, head) rows a unit at most.  cluster
+// > 0: that many blocks share a unit and no list or scratch is needed.
+constexpr int kFewBlock = 64;                      // keys a block of the share-out
+inline int few_rows(int cells) { return cells <= 8 ? 8 : cells <= 16 ? 16 : 32; }
+cudaError_t attend_few(const Attend& a, const mp_paged_cache& c, Work w, int cells, int cluster, cudaStream_t st);
+
+}  // namespace paged
+}  // namespace mp
