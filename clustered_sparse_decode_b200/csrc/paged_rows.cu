@@ -43,6 +43,9 @@ struct Few {
   Work w;
   int cluster;                                     // > 0: that many blocks share a unit and join in shared memory
 };
+// Up to this many requests every block makes the list itself, in shared memory
+// (a list kernel before it costs 5 us and a chain of dependent loads).
+constexpr int kOwnList = 512;
 
 template <typename T>
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -94,7 +97,10 @@ struct FewCfg {
   static constexpr int OFF_ML = OFF_BAR + kFewWarps * NS * 8;         // [warps][2][ROWS] maxima, sums
   static constexpr int OFF_UNIT = OFF_ML + kFewWarps * 2 * ROWS * 4;  // [2][ROWS] maxima, sums of the block
   static constexpr int OFF_BAD = OFF_UNIT + 2 * ROWS * 4;             // [ROWS] rows to be done again
-  static constexpr int USED = OFF_BAD + ROWS * 4;
+  static constexpr int OFF_LIST = (OFF_BAD + ROWS * 4 + 7) / 8 * 8;   // [kOwnList + 1] blocks before each request
+  static constexpr int OFF_KEY = OFF_LIST + (kOwnList + 1) * 8;       // [kOwnList] first keys
+  static constexpr int OFF_SUM = OFF_KEY + kOwnList * 4;              // [warps] sums
+  static constexpr int USED = OFF_SUM + kFewWarps * 8;
   static constexpr int SMEM = USED + 1024;                            // room to align
   static_assert(ROWS * PITCH * 4 <= kRing, "a warp's numerators fit its ring");
   static_assert(2 * SMEM <= 227 * 1024, "two blocks an SM");
@@ -127,15 +133,62 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) few_kernel(const __grid_con
   int64_t W = 0, x = 0, x1 = 0;
   int E = 0, N = 1, e = 0;
   const int part = f.cluster ? (int)(blockIdx.x % f.cluster) : (int)blockIdx.x;
+  const bool own = a.batch <= kOwnList;
+  const int64_t* before = own ? reinterpret_cast<const int64_t*>(smem + C::OFF_LIST) : f.w.before;
+  const int32_t* own_k0 = reinterpret_cast<const int32_t*>(smem + C::OFF_KEY);
   if (!f.cluster) {
-    E = f.w.count[0];
-    W = f.w.before[E] * a.H;
+    if (own) {
+      int64_t* sum = reinterpret_cast<int64_t*>(smem + C::OFF_SUM);
+      int64_t done = 0;
+      for (int b0 = 0; b0 < a.batch; b0 += kFewWarps * 32) {
+        const int b = b0 + tid;
+        Entry en{b, 0, 0, 0};
+        if (b < a.batch) {
+          const Request r = request_of(a, b);
+          if (r.n > 0) span_of(a, r, b, 0, r.n, kFewBlock, en);
+        }
+        int64_t s = en.n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t y = __shfl_up_sync(kFull, s, o);
+          if (lane >= o) s += y;
+        }
+        if (lane == 31) sum[warp] = s;
+        __syncthreads();
+        int64_t at = done;
+        for (int w = 0; w < kFewWarps; ++w) {
+          if (w < warp) at += sum[w];
+          done += sum[w];
+        }
+        if (b < a.batch) {
+          const_cast<int64_t*>(before)[b] = at + s - en.n;
+          const_cast<int32_t*>(own_k0)[b] = en.k0;
+          if (part == 0) {             // for the joining kernel
+            f.w.before[b] = at + s - en.n;
+            f.w.entry[b] = en;
+          }
+        }
+        __syncthreads();
+      }
+      if (tid == 0) {
+        const_cast<int64_t*>(before)[a.batch] = done;
+        if (part == 0) {
+          f.w.before[a.batch] = done;
+          f.w.count[0] = a.batch;
+        }
+      }
+      __syncthreads();
+    }
+    E = own ? a.batch : f.w.count[0];
+    W = E > 0 ? before[E] * a.H : 0;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (W == 0) return;
     N = parts_used(f.w, W);
-    if (E == 0 || part >= N) return;
+    if (part >= N) return;
     x = share(W, N, part);
     x1 = share(W, N, part + 1);
     if (x >= x1) return;
-    e = entry_of(f.w, E, a.H, x);
+    e = entry_of(before, E, a.H, x);
   } else {
     x1 = 1;
   }
@@ -152,15 +205,15 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) few_kernel(const __grid_con
       b = u / a.H;
       h = u - b * a.H;
     } else {
-      while (f.w.before[e + 1] * a.H <= x) ++e;
-      const int64_t n = f.w.before[e + 1] - f.w.before[e], first = f.w.before[e] * a.H;
-      b = f.w.entry[e].b;
+      while (before[e + 1] * a.H <= x) ++e;      // requests without rows have no blocks
+      const int64_t n = before[e + 1] - before[e], first = before[e] * a.H;
+      b = own ? e : f.w.entry[e].b;
       h = (int)((x - first) / n);
       u0 = first + h * n;
       u1 = u0 + n;
       blk0 = (int)(x - u0);
       blk1 = (int)(min(x1, u1) - u0);
-      k0 = f.w.entry[e].k0;
+      k0 = own ? own_k0[e] : f.w.entry[e].k0;
     }
     const Request r = request_of(a, b);
     const int prefix = prefix_of(a, b), cells = r.n * a.G;
@@ -481,12 +534,12 @@ static cudaError_t launch_few_t(Few& f, int units, cudaStream_t st) {
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = f.cluster;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  } else {                             // the list kernel lies before it
+  } else if (f.a.batch > kOwnList) {   // the list kernel lies before it
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
   }
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = f.cluster || f.a.batch > kOwnList ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kern, (const Few)f);
 }
 
@@ -515,7 +568,7 @@ cudaError_t attend_few(const Attend& a, const mp_paged_cache& c, Work w, int cel
   const int D = c.cfg.head_dim;
   if (cluster) return launch_few(f, c.cfg.dtype, D, cells, a.batch * a.H, st);
   f.w = w;
-  cudaError_t e = launch_work(a, w, a.max_new, kFewBlock, st);
+  cudaError_t e = a.batch > kOwnList ? launch_work(a, w, a.max_new, kFewBlock, st) : cudaSuccess;
   if (e == cudaSuccess) e = launch_few(f, c.cfg.dtype, D, cells, a.batch * a.H, st);
   if (e == cudaSuccess) e = launch_join(a, w, c.cfg.dtype, D, a.max_new, few_rows(cells), a.batch, st);
   return e;

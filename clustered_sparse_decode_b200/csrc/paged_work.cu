@@ -59,24 +59,8 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const Attend a, cons
     if (e < E) {
       Entry x = w.entry[e];
       const Request r = request_of(a, x.b);
-      const int prefix = prefix_of(a, x.b);
-      int lo = INT32_MAX, hi = 0;
-      const int i0 = x.tile * tile, i1 = min(r.n, i0 + tile);
-      if (a.first_key) {                       // in any order: every row counts
-        for (int i = i0; i < i1; ++i) {
-          const Interval v = interval_of(a, r, prefix, i);
-          if (v.hi > v.lo) { lo = min(lo, v.lo); hi = max(hi, v.hi); }
-        }
-      } else {                                 // the ends move with the rows
-        for (int i = i0; i < i1; i += max(1, i1 - 1 - i0)) {
-          const Interval v = interval_of(a, r, prefix, i);
-          lo = min(lo, v.lo);
-          hi = max(hi, v.hi);
-        }
-      }
-      x.k0 = hi > lo ? lo / block * block : 0;
-      // rows that see nothing cost a block: their zeros are written
-      n = x.n = hi > lo ? (hi - x.k0 + block - 1) / block : 1;
+      span_of(a, r, x.b, x.tile * tile, min(r.n, (x.tile + 1) * tile), block, x);
+      n = x.n;
       w.entry[e] = x;
     }
     const int64_t at = scan(n);
@@ -85,38 +69,75 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const Attend a, cons
   if (tid == 0) w.before[E] = carry;
 }
 
-// A block joins one row of one unit; thread c its column c.
+// A block joins one row of one unit: first all parts' maxima and sums side by
+// side, then thread c adds up its column c, eight parts' loads in flight (one
+// after the other they took three times as long: 16.8 us against 5 for the 38
+// parts of 64K tokens on 8 heads).
 template <typename T, int D>
 __global__ void __launch_bounds__(D) join_kernel(const Attend a, const Work w, int tile, int rows) {
+  __shared__ float weight[kMostParts];
+  __shared__ float red[2][D / 32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int E = w.count[0], e = blockIdx.x / a.H, h = blockIdx.x % a.H;
+  const int E = w.count[0], e = blockIdx.x / a.H, h = blockIdx.x % a.H, tid = threadIdx.x;
   if (e >= E) return;
   const int64_t W = w.before[E] * a.H, n = w.before[e + 1] - w.before[e], u0 = w.before[e] * a.H + h * n, u1 = u0 + n;
-  const int N = parts_used(w, W), c0 = part_of(W, N, u0), c1 = part_of(W, N, u1 - 1);
-  if (c0 == c1) return;                        // the part wrote the result itself
+  if (n == 0) return;                          // a request without rows
   const Entry x = w.entry[e];
+  const int N = parts_used(w, W), c0 = part_of(W, N, u0), c1 = part_of(W, N, u1 - 1), np = c1 - c0 + 1;
+  if (np == 1) return;                         // the part wrote the result itself
   const Request r = request_of(a, x.b);
   const int cells = min(tile, r.n - x.tile * tile) * a.G;
   const bool inside = share(W, N, c0) < u0;    // part c0 began with another unit
   const int64_t size = (int64_t)rows * (2 + D);
+  const float* p0 = w.part + (2 * (int64_t)c0 + (inside ? 1 : 0)) * size;
+  const float* p1 = w.part + 2 * (int64_t)(c0 + 1) * size;             // parts behind c0 begin inside the unit
+  auto slot = [&](int i) { return i == 0 ? p0 : p1 + 2 * (int64_t)(i - 1) * size; };
   for (int row = blockIdx.y; row < cells; row += gridDim.y) {
-    auto slot = [&](int c) { return w.part + (2 * (int64_t)c + (c == c0 && inside ? 1 : 0)) * size; };
     float m = -INFINITY;
-    for (int c = c0; c <= c1; ++c) m = fmaxf(m, slot(c)[row]);
-    float l = 0.f, o = 0.f;
-#pragma unroll 4
-    for (int c = c0; c <= c1; ++c) {
-      const float* p = slot(c);
-      const float mc = p[row], f = mc == -INFINITY ? 0.f : exp2f(mc - m), v = p[2 * rows + row * D + threadIdx.x];
-      l = fmaf(f, p[rows + row], l);
-      if (f != 0.f) o = fmaf(f, v, o);         // a part that saw nothing holds no numerator
+    for (int i = tid; i < np; i += D) {
+      weight[i] = slot(i)[row];
+      m = fmaxf(m, weight[i]);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+    if ((tid & 31) == 0) red[0][tid >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) m = fmaxf(m, red[0][i]);
+    float l = 0.f;
+    for (int i = tid; i < np; i += D) {
+      const float f = weight[i] == -INFINITY ? 0.f : exp2f(weight[i] - m);
+      weight[i] = f;
+      l = fmaf(f, slot(i)[rows + row], l);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(kFull, l, o);
+    if ((tid & 31) == 0) red[1][tid >> 5] = l;
+    __syncthreads();
+    l = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) l += red[1][i];
+    float o = 0.f;
+    int i = 0;
+    for (; i + 8 <= np; i += 8) {
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = slot(i + k)[2 * rows + row * D + tid];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (weight[i + k] != 0.f) o = fmaf(weight[i + k], v[k], o);    // a part that saw nothing holds no numerator
+    }
+    for (; i < np; ++i) {
+      const float v = slot(i)[2 * rows + row * D + tid];
+      if (weight[i] != 0.f) o = fmaf(weight[i], v, o);
     }
     const bool none = l == 0.f;
     const int t = r.row0 + x.tile * tile + row / a.G, hq = h * a.G + row % a.G;
     T* dst = reinterpret_cast<T*>(a.O + (int64_t)t * a.o_row_b + (int64_t)hq * a.o_head_b);
-    dst[threadIdx.x] = from_f32<T>(none ? 0.f : o / l);
-    if (a.lse && threadIdx.x == 0)
+    dst[tid] = from_f32<T>(none ? 0.f : o / l);
+    if (a.lse && tid == 0)
       a.lse[(int64_t)t * a.H * a.G + hq] = none ? -INFINITY : (m + log2f(l)) / kLog2e;
+    __syncthreads();
   }
 }
 

@@ -42,14 +42,35 @@ __device__ __forceinline__ int part_of(int64_t W, int N, int64_t x) {
   return c;
 }
 // the entry that block x of the line belongs to
-__device__ __forceinline__ int entry_of(const Work& w, int E, int H, int64_t x) {
+__device__ __forceinline__ int entry_of(const int64_t* before, int E, int H, int64_t x) {
   int lo = 0, hi = E;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (w.before[mid] * H <= x) lo = mid;
+    if (before[mid] * H <= x) lo = mid;
     else hi = mid;
   }
   return lo;
+}
+
+constexpr int kMostParts = 2 * 148;
+
+// The blocks of keys that rows [i0, i1) of a request see together.  Rows that
+// see nothing cost a block: their zeros are written.
+__device__ __forceinline__ void span_of(const Attend& a, const Request& r, int b, int i0, int i1, int block, Entry& x) {
+  const int prefix = prefix_of(a, b);
+  int lo = INT32_MAX, hi = 0;
+  if (a.first_key) {                   // in any order: every row counts
+    for (int i = i0; i < i1; ++i) {
+      const Interval v = interval_of(a, r, prefix, i);
+      if (v.hi > v.lo) { lo = min(lo, v.lo); hi = max(hi, v.hi); }
+    }
+  } else if (i0 < i1) {                // the ends move with the rows
+    const Interval v = interval_of(a, r, prefix, i0), z = interval_of(a, r, prefix, i1 - 1);
+    lo = min(v.lo, z.lo);
+    hi = max(v.hi, z.hi);
+  }
+  x.k0 = hi > lo ? lo / block * block : 0;
+  x.n = hi > lo ? (hi - x.k0 + block - 1) / block : 1;
 }
 
 // Makes the list: tiles of `tile` rows (tokens), blocks of `block` keys.
