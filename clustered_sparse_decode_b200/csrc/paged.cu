@@ -1,14 +1,12 @@
 // Paged cache: handle, step addresses, appending, gathering (attention in
 // paged_attend.cu).
 #include <cooperative_groups.h>
-#include <cudaTypedefs.h>
-
 #include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <mutex>
 
-#include "paged_common.cuh"
+#include "paged_work.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -257,7 +255,7 @@ static int log2_of(int x) {
   return s;
 }
 
-static PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -273,7 +271,7 @@ static PFN_cuTensorMapEncodeTiled_v12000 encoder() {
 // K or V as [page][head][64-column panel][token][64 columns], 128-byte
 // swizzle; a box is `rows` tokens of one head's page, one panel or all.
 static bool encode_pages(uint64_t* out, const mp_paged_cache& c, void* base, int rows, int panels) {
-  auto fn = encoder();
+  auto fn = map_encoder();
   if (!fn) return false;
   const mp_paged_config& g = c.cfg;
   CUtensorMap tm;

@@ -94,20 +94,29 @@ static void launch_plain(const Attend& a, int D, cudaStream_t st) {
 // How a call is done.  Few (token, head) rows a KV head: paged_rows.cu, blocks
 // in clusters of one unit (one launch) while a block's part of the longest
 // request that the table can hold stays short, shares over all SMs otherwise
-// (three launches, the same time whatever the lengths).
+// (two or three launches, the same time whatever the lengths).  More rows:
+// paged_tiles.cu.  fp32: row by row.
 constexpr int kFewCells = 32;          // rows that the few-rows kernel takes
-constexpr int kFewParts = 2 * 148;     // two blocks an SM
+constexpr int kFewParts = kMostParts;  // two blocks an SM
+constexpr int kTilesParts = 148;       // one
 constexpr int kClusterBlocks = 16;     // blocks of keys of a clustered block at most
 
 struct Way {
-  bool few;
+  bool few, tiles;
   int cells, cluster, entries, rows, parts;
 };
 
 static Way way_of(const mp_paged_cache& c, const mp_paged_attend_args& p) {
   Way w{};
   const int G = p.q_heads / c.cfg.kv_heads, max_new = p.max_new ? p.max_new : p.rows;
-  if (c.cfg.dtype == MP_F32 || (int64_t)max_new * G > kFewCells) return w;
+  if (c.cfg.dtype == MP_F32) return w;
+  if ((int64_t)max_new * G > kFewCells) {
+    w.tiles = true;
+    w.entries = p.rows / tiles_tokens(G) + p.batch;
+    w.rows = kTilesRows;
+    w.parts = kTilesParts;
+    return w;
+  }
   w.few = true;
   w.cells = max_new * G;
   const int64_t units = (int64_t)p.batch * c.cfg.kv_heads;
@@ -159,21 +168,20 @@ mp_status paged_attend_impl(const mp_paged_cache& c, const mp_paged_attend_args&
   const paged::Attend a = paged::args_of(c, p);
   const paged::Way w = paged::way_of(c, p);
   cudaError_t e = cudaSuccess;
+  paged::Work work{};
+  paged::lay_work(w, c.cfg.head_dim, scratch, &work);
   if (w.few) {
-    paged::Work work{};
-    paged::lay_work(w, c.cfg.head_dim, scratch, &work);
     work.least = 4;
     e = paged::attend_few(a, c, work, w.cells, w.cluster, st);
-  } else if (c.cfg.dtype == MP_F32) {
-    paged::launch_plain<float>(a, c.cfg.head_dim, st);
-  } else if (c.cfg.dtype == MP_BF16) {
-    paged::launch_plain<__nv_bfloat16>(a, c.cfg.head_dim, st);
+  } else if (w.tiles) {
+    work.least = 4;
+    e = paged::attend_tiles(a, c, work, w.entries, st);
   } else {
-    paged::launch_plain<__half>(a, c.cfg.head_dim, st);
+    paged::launch_plain<float>(a, c.cfg.head_dim, st);
   }
   if (e == cudaSuccess) return cudaGetLastError() == cudaSuccess ? MP_OK : MP_ECUDA;
   cudaGetLastError();
-  return MP_ECUDA;
+  return e == cudaErrorNotSupported ? MP_EUNSUPPORTED : MP_ECUDA;
 }
 
 }  // namespace mp

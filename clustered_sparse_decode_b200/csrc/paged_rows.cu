@@ -570,7 +570,7 @@ cudaError_t attend_few(const Attend& a, const mp_paged_cache& c, Work w, int cel
   f.w = w;
   cudaError_t e = a.batch > kOwnList ? launch_work(a, w, a.max_new, kFewBlock, st) : cudaSuccess;
   if (e == cudaSuccess) e = launch_few(f, c.cfg.dtype, D, cells, a.batch * a.H, st);
-  if (e == cudaSuccess) e = launch_join(a, w, c.cfg.dtype, D, a.max_new, few_rows(cells), a.batch, st);
+  if (e == cudaSuccess) e = launch_join(a, w, c.cfg.dtype, D, a.max_new, few_rows(cells), st);
   return e;
 }
 

@@ -1,0 +1,624 @@
+// Attention over a paged cache for requests with many rows (prompts' chunks):
+// 16-bit types, tensor cores with accumulators in tensor memory.
+//
+// The G query heads of a KV head are rows of the same tile, (token, head) pairs
+// in that order: a tile holds 256 rows, 256 / G tokens, as two halves of 128
+// that read the same keys.  Blocks of 128 keys and values pass through a ring
+// of shared-memory stages, one TMA box a page and 64-column panel.  Per block
+// and half
+//   S = Q K^T        (tcgen05.mma, 128 x 128 fp32 in tensor memory)
+//   P = 2^(S c - m)  (a thread a row: no exchange between threads)
+//   O += P V         (tcgen05.mma with P read from tensor memory, where it has
+//                     taken the place of S; O stays in tensor memory)
+// One warp issues all products, one all loads, and a group of four warps does
+// the softmax of each half.  The halves alternate: while one group works on its
+// S, the tensor cores do the other half's two products.  They need 2 x 512
+// cycles a half and block at head dim 128, the exponentials 1024 a half: both
+// units are the bound, about equally.
+//
+// The running maximum is lazy (it moves when a score exceeds it by more than 8
+// in base 2), so that O is rarely read back and rescaled; the sums use the
+// weights before they are rounded to the values' type for the second product.
+// Keys that a row does not see have weight exactly 0; values behind a request's
+// last token are zeroed in shared memory, and a row whose result is not finite
+// is done again key by key, since a value that it does not see may have been
+// infinite or NaN.
+#include <cudaTypedefs.h>
+
+#include <cstring>
+#include <type_traits>
+
+#include "paged_work.cuh"
+#include "stream_common.cuh"
+
+namespace mp {
+namespace paged {
+
+constexpr int kHalf = 128;                         // rows of a half (MMA M)
+constexpr int kKeys = kTilesBlock;                 // keys a block (MMA N, then K)
+constexpr int kTilesThreads = 384;                 // 2 x 4 softmax warps, MMA, load, two idle
+constexpr int kSoftRegs = 208, kRestRegs = 88;     // 256 * 208 + 128 * 88 <= 384 * 168
+
+struct Tiles {
+  CUtensorMap tmQ, tmK, tmV;
+  Attend a;
+  Work w;
+  int tile;                                        // tokens a tile
+  int box;                                         // tokens a K or V box
+};
+
+template <int D>
+struct TilesCfg {
+  static constexpr int KT = D / 64;                                   // 64-column panels
+  static constexpr int PANEL = kKeys * 128;                           // bytes of a panel of 128 rows
+  static constexpr int STAGE = KT * PANEL;
+  static constexpr int NS = 160 * 1024 / STAGE;
+  static constexpr int OFF_Q = 0;                                     // [2 halves][KT][128 rows][128 B]
+  static constexpr int OFF_KV = 2 * STAGE;                            // [NS][KT][128 rows][128 B]
+  static constexpr int OFF_BAR = OFF_KV + NS * STAGE;
+  static constexpr int BARS = 2 * NS + 9;
+  static constexpr int USED = OFF_BAR + BARS * 8 + 16;
+  static constexpr int SMEM = USED + 1024;
+  static_assert(SMEM <= 232448, "shared memory of a block");
+};
+
+// ---------------------------------------------------------------------------
+// tcgen05
+// ---------------------------------------------------------------------------
+// Shared-memory descriptors, 128-byte swizzle, version 1.  K-major (Q, K): rows
+// of 128 bytes, groups of 8 rows 1024 bytes apart; 16 elements along K are 32
+// bytes.  MN-major (V as [keys][columns]): groups of 8 keys 1024 bytes apart,
+// the next 64 columns a panel further; 16 keys are 2048 bytes.
+__device__ __forceinline__ uint64_t desc_base(int leading, int stride) {
+  return ((uint64_t)(leading >> 4) << 16) | ((uint64_t)(stride >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+__device__ __forceinline__ uint64_t desc_at(uint64_t base, uint32_t addr) {
+  return base | (uint64_t)((addr >> 4) & 0x3FFFu);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t idesc(int n, bool v_major) {
+  const uint32_t f = std::is_same<T, __half>::value ? 0u : 1u;
+  return (1u << 4) | (f << 7) | (f << 10) | (v_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
+         ((uint32_t)(kHalf >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t da, uint64_t db, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(da), "l"(db), "r"(id), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t ta, uint64_t db, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(ta), "l"(db), "r"(id), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
+// 32 columns of this thread's lane; the values are there after tmem_ld_wait
+__device__ __forceinline__ void tmem_ld(uint32_t at, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(at));
+}
+// waits for this warp's loads; 32 loaded values pass through, so that no use of them can move before it
+__device__ __forceinline__ void tmem_ld_wait(float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]),
+                 "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]),
+                 "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]),
+                 "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};\n" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(at)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+
+__device__ __forceinline__ void tma_kv(uint32_t dst, const CUtensorMap* tm, int row, int panel, int head, int page,
+                                       uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, "
+      "%6}], [%7];\n" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tm)), "r"(0), "r"(row), "r"(panel), "r"(head),
+      "r"(page), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_q(uint32_t dst, const CUtensorMap* tm, int col, int head, int row, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];\n" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tm)), "r"(col), "r"(head), "r"(row), "r"(bar)
+      : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// A block's items: the units, or parts of units, of its share
+// ---------------------------------------------------------------------------
+struct Item {
+  int b, h, i0;                        // request, KV head, first token of the tile in the request
+  Request r;
+  int key0, nb;                        // first key, blocks
+  int from[2], to[2];                  // blocks that each half's rows can see ([0, 0): none)
+  bool whole, head;                    // the unit is not cut; the share begins with this item
+  int64_t next;
+};
+
+struct Walk {
+  int64_t x, x1, start;
+  int e;
+};
+
+// The next item, or false at the share's end.  All lanes of a warp together.
+__device__ __forceinline__ bool next_item(const Tiles& f, Walk& w, Item& it) {
+  if (w.x >= w.x1) return false;
+  const Attend& a = f.a;
+  const int lane = threadIdx.x & 31;
+  while (f.w.before[w.e + 1] * a.H <= w.x) ++w.e;
+  const int64_t first = f.w.before[w.e] * a.H, n = f.w.before[w.e + 1] - f.w.before[w.e];
+  const Entry en = f.w.entry[w.e];
+  it.b = en.b;
+  it.h = (int)((w.x - first) / n);
+  const int64_t u0 = first + it.h * n, u1 = u0 + n, end = min(w.x1, u1);
+  it.i0 = en.tile * f.tile;
+  it.r = request_of(a, en.b);
+  it.key0 = en.k0 + (int)(w.x - u0) * kKeys;
+  it.nb = (int)(end - w.x);
+  it.whole = w.x == u0 && end == u1;
+  it.head = w.x == w.start;
+  const int prefix = prefix_of(a, en.b);
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    int lo = INT32_MAX, hi = 0;
+    const int i0 = it.i0 + g * (f.tile / 2), i1 = min(it.r.n, i0 + f.tile / 2);
+    for (int i = i0 + lane; i < i1; i += 32) {
+      const Interval v = interval_of(a, it.r, prefix, i);
+      if (v.hi > v.lo) {
+        lo = min(lo, v.lo);
+        hi = max(hi, v.hi);
+      }
+    }
+    lo = __reduce_min_sync(kFull, lo);
+    hi = __reduce_max_sync(kFull, hi);
+    it.from[g] = hi > lo ? max(0, min(it.nb, (lo - it.key0) >> 7)) : 0;
+    it.to[g] = hi > lo ? max(0, min(it.nb, (hi - it.key0 + kKeys - 1) >> 7)) : 0;
+    if (it.to[g] <= it.from[g]) it.from[g] = it.to[g] = 0;
+  }
+  w.x = end;
+  return true;
+}
+
+// One row done again, out of line: it is rare and needs registers.
+template <typename T, int D>
+__device__ __noinline__ void row_again(const Attend* a, int b, const Request* r, int i, int hq, int k0, int k1, bool whole,
+                                       float* m, float* l, float* num) {
+  RowState<T, D> s;
+  attend_row<T, D>(*a, b, *r, i, hq, k0, k1, s);
+  const int lane = threadIdx.x & 31;
+  if (whole) {
+    T* o = reinterpret_cast<T*>(a->O + (int64_t)(r->row0 + i) * a->o_row_b + (int64_t)hq * a->o_head_b) + lane * (D / 32);
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) o[e] = from_f32<T>(s.l == 0.f ? 0.f : s.acc[e] / s.l);
+    if (a->lse && lane == 0)
+      a->lse[(int64_t)(r->row0 + i) * a->H * a->G + hq] = s.l == 0.f ? -INFINITY : (s.m + log2f(s.l)) / kLog2e;
+  } else {
+    if (lane == 0) { *m = s.m; *l = s.l; }
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) num[lane * (D / 32) + e] = s.acc[e];
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t to_pair(float lo, float hi) {
+  if constexpr (std::is_same<T, __half>::value) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    return sc::pack_bf16(lo, hi);
+  }
+}
+
+// GEN: scores are capped or biased, or the scale is negative: the exponent is
+// formed first, and its factor is 1.
+template <typename T, int D, bool GEN>
+__global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_constant__ Tiles f) {
+  using C = TilesCfg<D>;
+  constexpr int NS = C::NS, KT = C::KT;
+  const Attend& a = f.a;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024u - (sc::smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sb = sc::smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t kv_full = sb + C::OFF_BAR, kv_empty = kv_full + 8 * NS, q_full = kv_empty + 8 * NS, q_empty = q_full + 8,
+                 s_full = q_empty + 8, p_full = s_full + 16, o_full = p_full + 16, drain = o_full + 16;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + C::BARS * 8);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      sc::mbar_init(kv_full + 8 * s, 1);
+      sc::mbar_init(kv_empty + 8 * s, 1);
+    }
+    sc::mbar_init(q_full, 1);
+    sc::mbar_init(q_empty, 1);
+    sc::mbar_init(drain, 1);
+    for (int g = 0; g < 2; ++g) {
+      sc::mbar_init(s_full + 8 * g, 1);
+      sc::mbar_init(p_full + 8 * g, 4);
+      sc::mbar_init(o_full + 8 * g, 1);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(sc::smem_u32(tmem_slot)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = *tmem_slot;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // this block's share
+  const int E = f.w.count[0];
+  const int64_t W = E > 0 ? f.w.before[E] * a.H : 0;
+  const int N = W > 0 ? parts_used(f.w, W) : 0, part = blockIdx.x;
+  Walk walk{0, 0, 0, 0};
+  if (part < N) {
+    walk.x = walk.start = share(W, N, part);
+    walk.x1 = share(W, N, part + 1);
+    if (walk.x < walk.x1) walk.e = entry_of_warp(f.w.before, E, a.H, walk.x);
+  }
+  Item it;
+  bool ok = true;
+  auto wait = [&](uint32_t bar, uint32_t parity) {       // two seconds at most; after one failure at once
+    if (ok && !sc::mbar_try(bar, parity) && !sc::mbar_wait(bar, parity, sc::gtimer() + 2000000000LL)) {
+      ok = false;
+      set_error(a.err, E_TIMEOUT);
+    }
+    ok = __all_sync(kFull, ok);
+    return ok;
+  };
+
+  if (warp < 8) {
+    // ================= softmax: a thread a row =================
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftRegs));
+    const int g = warp >> 2, row = threadIdx.x & 127;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t tS = tmem + 128 * g + lanes, tO = tmem + 256 + 128 * g + lanes;
+    const float c = GEN ? 1.f : a.scale * kLog2e;
+    uint32_t n_s = 0, n_o = 0, n_kv = 0;                 // phases of s_full and o_full, tiles that have passed the ring
+    while (ok && next_item(f, walk, it)) {
+      const int i = it.i0 + g * (f.tile / 2) + row / a.G, hq = it.h * a.G + row % a.G;
+      const bool valid = i < it.r.n;
+      Interval v{0, INT32_MAX, 0};
+      if (valid) v = interval_of(a, it.r, prefix_of(a, it.b), i);
+      const float slope = GEN && a.slopes ? __ldg(a.slopes + hq) * kLog2e : 0.f;
+      float m = -INFINITY, l = 0.f;
+      for (int j = it.from[g]; j < it.to[g]; ++j) {
+        if (!wait(s_full + 8 * g, n_s++ & 1u)) break;
+        tc_after();
+        float s[128];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tmem_ld(tS + 32 * k, s + 32 * k);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tmem_ld_wait(s + 32 * k);
+        const int kb = it.key0 + j * kKeys;
+        if (GEN) {
+#pragma unroll
+          for (int k = 0; k < 128; ++k) {
+            float z = s[k] * a.scale;
+            if (a.cap > 0.f) z = a.cap * (1.f - __fdividef(2.f, 1.f + sc::ex2(z * (2.f * kLog2e / a.cap))));
+            z *= kLog2e;
+            if (a.slopes) z -= slope * (float)abs(v.pos - kb - k);
+            s[k] = z;
+          }
+        }
+        if (__any_sync(kFull, v.lo > kb || v.hi < kb + kKeys)) {
+          const int lo = v.lo - kb, hi = v.hi - kb;
+#pragma unroll
+          for (int k = 0; k < 128; ++k)
+            if (k < lo || k >= hi) s[k] = -INFINITY;
+        }
+        float top[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int k = 4; k < 128; ++k) top[k & 3] = fmaxf(top[k & 3], s[k]);
+        const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
+        if (__any_sync(kFull, mx > m + 8.f)) {
+          const float nm = fmaxf(m, mx), keep = m == -INFINITY ? 0.f : sc::ex2(m - nm);
+          m = nm;
+          l *= keep;
+          if (j > it.from[g]) {                          // the numerator: its last product has ended with this S
+#pragma unroll 1
+            for (int k = 0; k < D; k += 32) {
+              float o[32];
+              tmem_ld(tO + k, o);
+              tmem_ld_wait(o);
+#pragma unroll
+              for (int q = 0; q < 32; ++q) o[q] *= keep;
+              tmem_st(tO + k, reinterpret_cast<const uint32_t*>(o));
+            }
+          }
+        }
+        const float base = m == -INFINITY ? 0.f : m;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t p[64];
+#pragma unroll
+        for (int k = 0; k < 64; ++k) {
+          const float p0 = sc::ex2(fmaf(s[2 * k], c, -base)), p1 = sc::ex2(fmaf(s[2 * k + 1], c, -base));
+          sum[k & 1] += p0;
+          sum[2 + (k & 1)] += p1;
+          p[k] = to_pair<T>(p0, p1);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_st(tS, p);
+        tmem_st(tS + 32, p + 32);
+        tmem_st_wait();
+        if (kb + kKeys > it.r.len && (g == 0 || j < it.from[0] || j >= it.to[0])) {
+          // values behind the last token: zeros (the second half's product follows the first's)
+          const uint32_t at = n_kv + 2 * j + 1, st = at % NS;
+          if (!wait(kv_full + 8 * st, (at / NS) & 1u)) break;
+          const int r0 = max(0, it.r.len - kb);
+          for (int x = r0 * 8 + row; x < kKeys * 8; x += 128)
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt)
+              *reinterpret_cast<uint4*>(smem + C::OFF_KV + st * C::STAGE + kt * C::PANEL + x * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
+          sc::fence_proxy_async();
+        }
+        tc_before();
+        __syncwarp();
+        if (lane == 0) sc::mbar_arrive(p_full + 8 * g);
+      }
+      if (!ok) break;
+      // --- the half's result
+      const bool none = it.to[g] == it.from[g];
+      float* slot = f.w.part + (2 * (int64_t)part + (it.head ? 0 : 1)) * (int64_t)(2 * kHalf) * (2 + D);
+      const int cell = g * kHalf + row;
+      float* num = slot + 2 * (2 * kHalf) + (int64_t)cell * D;
+      T* out = reinterpret_cast<T*>(a.O + (int64_t)(it.r.row0 + i) * a.o_row_b + (int64_t)hq * a.o_head_b);
+      if (!none) {
+        if (!wait(o_full + 8 * g, n_o++ & 1u)) break;
+        tc_after();
+      }
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      bool fine = l == l;
+#pragma unroll 1
+      for (int k = 0; k < D; k += 32) {
+        float o[32];
+        __syncwarp();
+        if (none) {
+#pragma unroll
+          for (int q = 0; q < 32; ++q) o[q] = 0.f;
+        } else {
+          tmem_ld(tO + k, o);
+          tmem_ld_wait(o);
+        }
+#pragma unroll
+        for (int q = 0; q < 32; ++q) fine &= fabsf(o[q]) <= 3.4028235e38f;
+        if (!valid) continue;
+        if (it.whole) {
+#pragma unroll
+          for (int q = 0; q < 32; q += 8) {
+            uint4 w;
+            w.x = to_pair<T>(o[q] * inv, o[q + 1] * inv);
+            w.y = to_pair<T>(o[q + 2] * inv, o[q + 3] * inv);
+            w.z = to_pair<T>(o[q + 4] * inv, o[q + 5] * inv);
+            w.w = to_pair<T>(o[q + 6] * inv, o[q + 7] * inv);
+            *reinterpret_cast<uint4*>(out + k + q) = w;
+          }
+        } else {
+#pragma unroll
+          for (int q = 0; q < 32; q += 4)
+            *reinterpret_cast<float4*>(num + k + q) = make_float4(o[q], o[q + 1], o[q + 2], o[q + 3]);
+        }
+      }
+      tc_before();
+      if (valid) {
+        if (it.whole) {
+          if (a.lse)
+            a.lse[(int64_t)(it.r.row0 + i) * a.H * a.G + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) / kLog2e;
+        } else {
+          slot[cell] = l == 0.f ? -INFINITY : m;
+          slot[2 * kHalf + cell] = l;
+        }
+      }
+      uint32_t again = __ballot_sync(kFull, valid && !fine);
+      while (again) {
+        const int src = __ffs(again) - 1;
+        again &= again - 1;
+        const int ri = __shfl_sync(kFull, i, src), rh = __shfl_sync(kFull, hq, src), rc = __shfl_sync(kFull, cell, src);
+        const Request r = it.r;
+        row_again<T, D>(&a, it.b, &r, ri, rh, it.key0, it.key0 + it.nb * kKeys, it.whole, slot + rc,
+                        slot + 2 * kHalf + rc, slot + 2 * (2 * kHalf) + (int64_t)rc * D);
+      }
+      if (it.to[0] > it.from[0] || it.to[1] > it.from[1]) n_kv += 2 * it.nb;
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRestRegs));
+    if (warp == 8) {
+      // ================= products (one thread) =================
+      const uint64_t dk = desc_base(16, 1024), dv = desc_base(C::PANEL, 1024);
+      const uint32_t id_s = idesc<T>(kKeys, false), id_o = idesc<T>(D, true);
+      uint32_t n_kv = 0, n_q = 0, n_p[2] = {0, 0};
+      while (ok && next_item(f, walk, it)) {
+        const bool used[2] = {it.to[0] > it.from[0], it.to[1] > it.from[1]};
+        if (used[0] || used[1]) {
+          if (!wait(q_full, n_q++ & 1u)) break;
+          for (int j = 0; j <= it.nb && ok; ++j) {
+            const uint32_t kt = n_kv + 2 * j, ks = kt % NS, vt = kt - 1, vs = vt % NS;   // K of block j, V of block j - 1
+            if (j > 0 && !wait(kv_full + 8 * vs, (vt / NS) & 1u)) break;
+            if (j < it.nb && !wait(kv_full + 8 * ks, (kt / NS) & 1u)) break;
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              if (j > it.from[g] && j <= it.to[g]) {     // O += P V of block j - 1
+                if (!wait(p_full + 8 * g, n_p[g]++ & 1u)) break;
+                tc_after();
+                if (lane == 0) {
+                  const uint32_t v0 = sb + C::OFF_KV + vs * C::STAGE;
+#pragma unroll
+                  for (int k = 0; k < kKeys / 16; ++k)
+                    mma_ts(tmem + 256 + 128 * g, tmem + 128 * g + 8 * k, desc_at(dv, v0 + 2048 * k), id_o,
+                           j - 1 > it.from[g] || k > 0 ? 1u : 0u);
+                  if (j == it.to[g]) commit(o_full + 8 * g);
+                }
+              }
+              if (j >= it.from[g] && j < it.to[g]) {     // S = Q K^T of block j
+                tc_after();
+                if (lane == 0) {
+                  const uint32_t q0 = sb + C::OFF_Q + g * C::STAGE, k0 = sb + C::OFF_KV + ks * C::STAGE;
+#pragma unroll
+                  for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = (k >> 2) * C::PANEL + (k & 3) * 32;
+                    mma_ss(tmem + 128 * g, desc_at(dk, q0 + off), desc_at(dk, k0 + off), id_s, k > 0 ? 1u : 0u);
+                  }
+                  commit(s_full + 8 * g);
+                }
+              }
+            }
+            if (!ok) break;
+            if (lane == 0) {
+              if (j > 0) commit(kv_empty + 8 * vs);
+              if (j < it.nb) commit(kv_empty + 8 * ks);
+              if (j == it.nb) commit(q_empty);
+            }
+            __syncwarp();
+          }
+          n_kv += 2 * it.nb;
+        }
+      }
+      if (!ok) {                                         // gave up: products under way end before the memory is freed
+        if (lane == 0) commit(drain);
+        sc::mbar_wait(drain, 0, sc::gtimer() + 200000000LL);
+      }
+    } else if (warp == 9) {
+      // ================= loads =================
+      uint32_t n_kv = 0, n_q = 0, issued = 0;
+      const int pg = 1 << a.page_shift, boxes = kKeys / f.box;
+      while (ok && next_item(f, walk, it)) {
+        const bool used[2] = {it.to[0] > it.from[0], it.to[1] > it.from[1]};
+        if (!used[0] && !used[1]) continue;
+        if (n_q > 0 && !wait(q_empty, (n_q - 1) & 1u)) break;
+        ++n_q;
+        if (lane == 0) {
+          sc::mbar_arrive_tx(q_full, (used[0] ? C::STAGE : 0) + (used[1] ? C::STAGE : 0));
+          for (int g = 0; g < 2; ++g)
+            for (int k = 0; k < KT && used[g]; ++k)
+              tma_q(sb + C::OFF_Q + g * C::STAGE + k * C::PANEL, &f.tmQ, 64 * k, it.h * a.G,
+                    it.r.row0 + it.i0 + g * (f.tile / 2), q_full);
+        }
+        for (int j = 0; j < it.nb && ok; ++j) {
+          // a lane a box: its keys' page (page 0 in the place of a bad one, whose result does not count)
+          const int key = it.key0 + j * kKeys + lane * f.box;
+          const bool mine = lane < boxes && key < it.r.len;
+          const int page = mine ? max(0, page_of(a, it.b, key)) : 0;
+          const uint32_t bytes = __popc(__ballot_sync(kFull, mine)) * (uint32_t)f.box * D * 2;
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            const uint32_t t = n_kv + 2 * j + kv, s = t % NS;
+            if (t >= NS && !wait(kv_empty + 8 * s, (t / NS - 1) & 1u)) break;
+            if (lane == 0) sc::mbar_arrive_tx(kv_full + 8 * s, bytes);
+            __syncwarp();
+            issued = t + 1;
+            if (mine) {
+              const uint32_t dst = sb + C::OFF_KV + s * C::STAGE + lane * f.box * 128;
+              for (int k = 0; k < (f.box == kKeys ? 1 : KT); ++k)
+                tma_kv(dst + k * C::PANEL, kv ? &f.tmV : &f.tmK, key & (pg - 1), k, it.h, page, kv_full + 8 * s);
+            }
+          }
+        }
+        n_kv += 2 * it.nb;
+      }
+      // copies under way land before the block ends (only after a wait that gave up are there any left)
+      if (!ok)
+        for (uint32_t t = issued > NS ? issued - NS : 0; t < issued; ++t)
+          if (!sc::mbar_wait(kv_full + 8 * (t % NS), (t / NS) & 1u, sc::gtimer() + 200000000LL)) break;
+    }
+  }
+  tc_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(512) : "memory");
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+template <typename T, int D, bool GEN>
+static cudaError_t launch_tiles_t(const Tiles& f, cudaStream_t st) {
+  using C = TilesCfg<D>;
+  auto kern = tiles_kernel<T, D, GEN>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)f.w.parts);
+  cfg.blockDim = dim3(kTilesThreads);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, f);
+}
+
+template <typename T, int D>
+static cudaError_t launch_tiles(const Tiles& f, cudaStream_t st) {
+  const bool gen = f.a.cap > 0.f || f.a.slopes || f.a.scale < 0.f;
+  return gen ? launch_tiles_t<T, D, true>(f, st) : launch_tiles_t<T, D, false>(f, st);
+}
+
+// Q as [row][head][d]: a box is one KV head's query heads of kHalf / G rows, 64
+// columns.  Rows past the tensor's end read as zeros.
+static bool encode_q(CUtensorMap* tm, const Attend& a, int dtype, int D) {
+  auto fn = map_encoder();
+  if (!fn) return false;
+  cuuint64_t gdim[3] = {(cuuint64_t)D, (cuuint64_t)a.H * a.G, (cuuint64_t)a.rows};
+  cuuint64_t gstride[2] = {(cuuint64_t)a.q_head_b, (cuuint64_t)a.q_row_b};
+  cuuint32_t box[3] = {64, (cuuint32_t)a.G, (cuuint32_t)(kHalf / a.G)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(tm, dtype == MP_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+            const_cast<char*>(a.Q), gdim, gstride, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t attend_tiles(const Attend& a, const mp_paged_cache& c, const Work& w, int entries, cudaStream_t st) {
+  Tiles f{};
+  const int D = c.cfg.head_dim;
+  memcpy(&f.tmK, c.maps + 16 * MAP_KPAGE, sizeof(CUtensorMap));
+  memcpy(&f.tmV, c.maps + 16 * MAP_VPAGE, sizeof(CUtensorMap));
+  if (!encode_q(&f.tmQ, a, c.cfg.dtype, D)) return cudaErrorNotSupported;
+  f.a = a;
+  f.w = w;
+  f.tile = tiles_tokens(a.G);
+  f.box = c.cfg.page_tokens < kKeys ? c.cfg.page_tokens : kKeys;
+  cudaError_t e = launch_work(a, w, f.tile, kKeys, st);
+  if (e != cudaSuccess) return e;
+  if (c.cfg.dtype == MP_F16) e = D == 128 ? launch_tiles<__half, 128>(f, st) : launch_tiles<__half, 64>(f, st);
+  else e = D == 128 ? launch_tiles<__nv_bfloat16, 128>(f, st) : launch_tiles<__nv_bfloat16, 64>(f, st);
+  if (e != cudaSuccess) return e;
+  return launch_join(a, w, c.cfg.dtype, D, f.tile, 2 * kHalf, st);
+}
+
+}  // namespace paged
+}  // namespace mp

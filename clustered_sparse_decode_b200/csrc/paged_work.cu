@@ -1,4 +1,6 @@
 // Work list of a split attention call, and the joining of its partial results.
+#include <type_traits>
+
 #include "paged_work.cuh"
 
 namespace mp {
@@ -53,15 +55,34 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const Attend a, cons
   __syncthreads();
   if (tid == 0) { carry = 0; w.count[0] = E; }
   __syncthreads();
+  if (a.first_key) {                           // every row counts: a warp an entry
+    for (int e = warp; e < E; e += kListThreads / 32) {
+      Entry x = w.entry[e];
+      const Request r = request_of(a, x.b);
+      const int prefix = prefix_of(a, x.b), i1 = min(r.n, (x.tile + 1) * tile);
+      int lo = INT32_MAX, hi = 0;
+      for (int i = x.tile * tile + lane; i < i1; i += 32) {
+        const Interval v = interval_of(a, r, prefix, i);
+        if (v.hi > v.lo) { lo = min(lo, v.lo); hi = max(hi, v.hi); }
+      }
+      lo = __reduce_min_sync(kFull, lo);
+      hi = __reduce_max_sync(kFull, hi);
+      set_span(x, lo, hi, block);
+      if (lane == 0) w.entry[e] = x;
+    }
+    __syncthreads();
+  }
   for (int e0 = 0; e0 < E; e0 += kListThreads) {
     const int e = e0 + tid;
     int n = 0;
     if (e < E) {
       Entry x = w.entry[e];
-      const Request r = request_of(a, x.b);
-      span_of(a, r, x.b, x.tile * tile, min(r.n, (x.tile + 1) * tile), block, x);
+      if (!a.first_key) {
+        const Request r = request_of(a, x.b);
+        span_of(a, r, x.b, x.tile * tile, min(r.n, (x.tile + 1) * tile), block, x);
+        w.entry[e] = x;
+      }
       n = x.n;
-      w.entry[e] = x;
     }
     const int64_t at = scan(n);
     if (e < E) w.before[e] = at;
@@ -69,75 +90,74 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const Attend a, cons
   if (tid == 0) w.before[E] = carry;
 }
 
-// A block joins one row of one unit: first all parts' maxima and sums side by
-// side, then thread c adds up its column c, eight parts' loads in flight (one
-// after the other they took three times as long: 16.8 us against 5 for the 38
-// parts of 64K tokens on 8 heads).
+// Joins the units that were cut.  Each is found at the first boundary between
+// parts that lies inside it (blockIdx.x: the part behind the boundary); a warp
+// takes a row: its lanes hold 32 parts' maxima and sums at a time, then every
+// lane adds up its columns, eight parts' loads in flight.
+constexpr int kJoinWarps = 4;
+
 template <typename T, int D>
-__global__ void __launch_bounds__(D) join_kernel(const Attend a, const Work w, int tile, int rows) {
-  __shared__ float weight[kMostParts];
-  __shared__ float red[2][D / 32];
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Attend a, const Work w, int tile, int rows) {
+  constexpr int E = D / 32;                    // columns a lane
+  using Vec = typename std::conditional<E == 4, float4, float2>::type;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int E = w.count[0], e = blockIdx.x / a.H, h = blockIdx.x % a.H, tid = threadIdx.x;
-  if (e >= E) return;
-  const int64_t W = w.before[E] * a.H, n = w.before[e + 1] - w.before[e], u0 = w.before[e] * a.H + h * n, u1 = u0 + n;
-  if (n == 0) return;                          // a request without rows
-  const Entry x = w.entry[e];
-  const int N = parts_used(w, W), c0 = part_of(W, N, u0), c1 = part_of(W, N, u1 - 1), np = c1 - c0 + 1;
-  if (np == 1) return;                         // the part wrote the result itself
-  const Request r = request_of(a, x.b);
-  const int cells = min(tile, r.n - x.tile * tile) * a.G;
-  const bool inside = share(W, N, c0) < u0;    // part c0 began with another unit
+  const int count = w.count[0], c = blockIdx.x + 1;
+  const int64_t W = count > 0 ? w.before[count] * a.H : 0;
+  if (W == 0) return;
+  const int N = parts_used(w, W);
+  if (c >= N) return;
+  const int64_t x = share(W, N, c), before = share(W, N, c - 1);
+  const int e = entry_of_warp(w.before, count, a.H, x);
+  const int64_t first = w.before[e] * a.H, n = w.before[e + 1] - w.before[e];
+  const int h = (int)((x - first) / n);
+  const int64_t u0 = first + h * n, u1 = u0 + n;
+  if (x == u0 || before > u0) return;          // a boundary between units, or not this unit's first
+  const int c1 = part_of(W, N, u1 - 1), np = c1 - c + 2;
+  const Entry en = w.entry[e];
+  const Request r = request_of(a, en.b);
+  const int cells = min(tile, r.n - en.tile * tile) * a.G, lane = threadIdx.x & 31;
   const int64_t size = (int64_t)rows * (2 + D);
-  const float* p0 = w.part + (2 * (int64_t)c0 + (inside ? 1 : 0)) * size;
-  const float* p1 = w.part + 2 * (int64_t)(c0 + 1) * size;             // parts behind c0 begin inside the unit
+  // part c - 1 holds the unit as its first item or as its last; later parts begin inside it
+  const float* p0 = w.part + (2 * (int64_t)(c - 1) + (before < u0 ? 1 : 0)) * size;
+  const float* p1 = w.part + 2 * (int64_t)c * size;
   auto slot = [&](int i) { return i == 0 ? p0 : p1 + 2 * (int64_t)(i - 1) * size; };
-  for (int row = blockIdx.y; row < cells; row += gridDim.y) {
+  for (int row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); row < cells; row += gridDim.y * kJoinWarps) {
     float m = -INFINITY;
-    for (int i = tid; i < np; i += D) {
-      weight[i] = slot(i)[row];
-      m = fmaxf(m, weight[i]);
-    }
+    for (int i = lane; i < np; i += 32) m = fmaxf(m, slot(i)[row]);
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-    if ((tid & 31) == 0) red[0][tid >> 5] = m;
-    __syncthreads();
+    float l = 0.f, acc[E];
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) m = fmaxf(m, red[0][i]);
-    float l = 0.f;
-    for (int i = tid; i < np; i += D) {
-      const float f = weight[i] == -INFINITY ? 0.f : exp2f(weight[i] - m);
-      weight[i] = f;
-      l = fmaf(f, slot(i)[rows + row], l);
+    for (int q = 0; q < E; ++q) acc[q] = 0.f;
+    for (int i0 = 0; i0 < np; i0 += 32) {
+      float f = 0.f;
+      if (i0 + lane < np) {
+        const float mi = slot(i0 + lane)[row];
+        f = mi == -INFINITY ? 0.f : exp2f(mi - m);
+        l = fmaf(f, slot(i0 + lane)[rows + row], l);
+      }
+      for (int k0 = 0; k0 < min(32, np - i0); k0 += 8) {
+        Vec v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          v[k] = *reinterpret_cast<const Vec*>(slot(min(i0 + k0 + k, np - 1)) + 2 * rows + (int64_t)row * D + lane * E);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float fk = __shfl_sync(kFull, f, k0 + k);          // 0 behind the last part
+          const float* vk = reinterpret_cast<const float*>(&v[k]);
+          if (fk != 0.f)                       // a part that saw nothing holds no numerator
+#pragma unroll
+            for (int q = 0; q < E; ++q) acc[q] = fmaf(fk, vk[q], acc[q]);
+        }
+      }
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(kFull, l, o);
-    if ((tid & 31) == 0) red[1][tid >> 5] = l;
-    __syncthreads();
-    l = 0.f;
+    const int t = r.row0 + en.tile * tile + row / a.G, hq = h * a.G + row % a.G;
+    T* dst = reinterpret_cast<T*>(a.O + (int64_t)t * a.o_row_b + (int64_t)hq * a.o_head_b) + lane * E;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) l += red[1][i];
-    float o = 0.f;
-    int i = 0;
-    for (; i + 8 <= np; i += 8) {
-      float v[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = slot(i + k)[2 * rows + row * D + tid];
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (weight[i + k] != 0.f) o = fmaf(weight[i + k], v[k], o);    // a part that saw nothing holds no numerator
-    }
-    for (; i < np; ++i) {
-      const float v = slot(i)[2 * rows + row * D + tid];
-      if (weight[i] != 0.f) o = fmaf(weight[i], v, o);
-    }
-    const bool none = l == 0.f;
-    const int t = r.row0 + x.tile * tile + row / a.G, hq = h * a.G + row % a.G;
-    T* dst = reinterpret_cast<T*>(a.O + (int64_t)t * a.o_row_b + (int64_t)hq * a.o_head_b);
-    dst[tid] = from_f32<T>(none ? 0.f : o / l);
-    if (a.lse && tid == 0)
-      a.lse[(int64_t)t * a.H * a.G + hq] = none ? -INFINITY : (m + log2f(l)) / kLog2e;
-    __syncthreads();
+    for (int q = 0; q < E; ++q) dst[q] = from_f32<T>(l == 0.f ? 0.f : acc[q] / l);
+    if (a.lse && lane == 0) a.lse[(int64_t)t * a.H * a.G + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) / kLog2e;
   }
 }
 
@@ -146,14 +166,12 @@ cudaError_t launch_work(const Attend& a, const Work& w, int tile, int block, cud
   return cudaGetLastError();
 }
 
-cudaError_t launch_join(const Attend& a, const Work& w, int dtype, int D, int tile, int rows, int max_entries,
-                        cudaStream_t st) {
+cudaError_t launch_join(const Attend& a, const Work& w, int dtype, int D, int tile, int rows, cudaStream_t st) {
+  if (w.parts < 2) return cudaSuccess;
   cudaLaunchConfig_t cfg{};
-  // rows of a unit over the grid's second axis, as many as keep the grid at a few blocks an SM
-  int y = 1;
-  while (y * 2 <= rows && (int64_t)max_entries * a.H * y < 1184) y *= 2;
-  cfg.gridDim = dim3((unsigned)(max_entries * a.H), (unsigned)y);
-  cfg.blockDim = dim3(D);
+  // four rows a warp of a large unit, one of a small
+  cfg.gridDim = dim3((unsigned)(w.parts - 1), (unsigned)(rows <= 32 ? (rows + kJoinWarps - 1) / kJoinWarps : rows / 16));
+  cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -10,6 +10,8 @@
 // result does not depend on timing.
 #pragma once
 
+#include <cudaTypedefs.h>
+
 #include "paged_common.cuh"
 
 namespace mp {
@@ -52,10 +54,27 @@ __device__ __forceinline__ int entry_of(const int64_t* before, int E, int H, int
   return lo;
 }
 
+// the same by the lanes of a warp together, 32 places a round
+__device__ __forceinline__ int entry_of_warp(const int64_t* before, int E, int H, int64_t x) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = E;
+  while (n > 1) {
+    const int step = (n + 31) / 32, at = lo + lane * step;
+    const int hits = __popc(__ballot_sync(kFull, lane * step < n && before[at] * H <= x));
+    lo += (hits - 1) * step;
+    n = min(step, n - (hits - 1) * step);
+  }
+  return lo;
+}
+
 constexpr int kMostParts = 2 * 148;
 
-// The blocks of keys that rows [i0, i1) of a request see together.  Rows that
-// see nothing cost a block: their zeros are written.
+// An entry's blocks from the keys [lo, hi) that its rows see together.  Rows
+// that see nothing cost a block: their zeros are written.
+__device__ __forceinline__ void set_span(Entry& x, int lo, int hi, int block) {
+  x.k0 = hi > lo ? lo / block * block : 0;
+  x.n = hi > lo ? (hi - x.k0 + block - 1) / block : 1;
+}
 __device__ __forceinline__ void span_of(const Attend& a, const Request& r, int b, int i0, int i1, int block, Entry& x) {
   const int prefix = prefix_of(a, b);
   int lo = INT32_MAX, hi = 0;
@@ -69,21 +88,28 @@ __device__ __forceinline__ void span_of(const Attend& a, const Request& r, int b
     lo = min(v.lo, z.lo);
     hi = max(v.hi, z.hi);
   }
-  x.k0 = hi > lo ? lo / block * block : 0;
-  x.n = hi > lo ? (hi - x.k0 + block - 1) / block : 1;
+  set_span(x, lo, hi, block);
 }
 
 // Makes the list: tiles of `tile` rows (tokens), blocks of `block` keys.
 cudaError_t launch_work(const Attend& a, const Work& w, int tile, int block, cudaStream_t st);
-// Joins the partial results of cut units: `rows` (token, head) rows a unit, G heads a token.
-cudaError_t launch_join(const Attend& a, const Work& w, int dtype, int D, int tile, int rows, int max_entries,
-                        cudaStream_t st);
+// Joins the partial results of cut units: `rows` (token, head) rows a unit, of `tile` tokens.
+cudaError_t launch_join(const Attend& a, const Work& w, int dtype, int D, int tile, int rows, cudaStream_t st);
 
 // Few rows (paged_rows.cu): `cells` (token, head) rows a unit at most.  cluster
 // > 0: that many blocks share a unit and no list or scratch is needed.
 constexpr int kFewBlock = 64;                      // keys a block of the share-out
 inline int few_rows(int cells) { return cells <= 8 ? 8 : cells <= 16 ? 16 : 32; }
 cudaError_t attend_few(const Attend& a, const mp_paged_cache& c, Work w, int cells, int cluster, cudaStream_t st);
+
+// Many rows (paged_tiles.cu).
+constexpr int kTilesBlock = 128;                   // keys a block of the share-out
+constexpr int kTilesRows = 256;                    // (token, head) rows a unit
+inline int tiles_tokens(int G) { return kTilesRows / G; }
+cudaError_t attend_tiles(const Attend& a, const mp_paged_cache& c, const Work& w, int entries, cudaStream_t st);
+
+// cuTensorMapEncodeTiled, or null (paged.cu).
+PFN_cuTensorMapEncodeTiled_v12000 map_encoder();
 
 }  // namespace paged
 }  // namespace mp
