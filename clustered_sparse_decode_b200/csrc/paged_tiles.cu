@@ -56,7 +56,7 @@ struct TilesCfg {
   static constexpr int OFF_Q = 0;                                     // [2 halves][KT][128 rows][128 B]
   static constexpr int OFF_KV = 2 * STAGE;                            // [NS][KT][128 rows][128 B]
   static constexpr int OFF_BAR = OFF_KV + NS * STAGE;
-  static constexpr int BARS = 2 * NS + 9;
+  static constexpr int BARS = 2 * NS + 11;
   static constexpr int USED = OFF_BAR + BARS * 8 + 16;
   static constexpr int SMEM = USED + 1024;
   static_assert(SMEM <= 232448, "shared memory of a block");
@@ -128,6 +128,13 @@ __device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t* r) {
       "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
       "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
       "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(at)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};\n" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(at)
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
@@ -223,6 +230,42 @@ __device__ __noinline__ void row_again(const Attend* a, int b, const Request* r,
   }
 }
 
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(*reinterpret_cast<uint64_t*>(&d))
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)), "l"(*reinterpret_cast<uint64_t*>(&c)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(*reinterpret_cast<uint64_t*>(&d))
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+template <int N>
+__device__ __forceinline__ float top_of(const float* v) {
+  float t[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+  for (int k = 4; k + 8 <= N; k += 8)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) t[q] = max3(t[q], v[k + 2 * q], v[k + 2 * q + 1]);
+#pragma unroll
+  for (int k = (N - 4) / 8 * 8 + 4; k < N; ++k) t[k & 3] = fmaxf(t[k & 3], v[k]);
+  return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+}
+
 template <typename T>
 __device__ __forceinline__ uint32_t to_pair(float lo, float hi) {
   if constexpr (std::is_same<T, __half>::value) {
@@ -245,7 +288,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
   const uint32_t sb = sc::smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t kv_full = sb + C::OFF_BAR, kv_empty = kv_full + 8 * NS, q_full = kv_empty + 8 * NS, q_empty = q_full + 8,
-                 s_full = q_empty + 8, p_full = s_full + 16, o_full = p_full + 16, drain = o_full + 16;
+                 s_full = q_empty + 8, p_full = s_full + 16, o_full = p_full + 32, drain = o_full + 16;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + C::BARS * 8);
 
   if (threadIdx.x == 0) {
@@ -258,7 +301,8 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
     sc::mbar_init(drain, 1);
     for (int g = 0; g < 2; ++g) {
       sc::mbar_init(s_full + 8 * g, 1);
-      sc::mbar_init(p_full + 8 * g, 4);
+      sc::mbar_init(p_full + 16 * g, 4);                 // the first 64 keys' weights, the last's
+      sc::mbar_init(p_full + 16 * g + 8, 4);
       sc::mbar_init(o_full + 8 * g, 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -303,7 +347,8 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
     const int g = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t tS = tmem + 128 * g + lanes, tO = tmem + 256 + 128 * g + lanes;
-    const float c = GEN ? 1.f : a.scale * kLog2e;
+    const float c = a.scale * kLog2e;
+    const float cap2 = a.cap * kLog2e, cap_in = GEN && a.cap > 0.f ? 2.f * c / a.cap : 0.f;   // cap tanh(z / cap) = cap - 2 cap / (1 + e^(2 z / cap))
     uint32_t n_s = 0, n_o = 0, n_kv = 0;                 // phases of s_full and o_full, tiles that have passed the ring
     while (ok && next_item(f, walk, it)) {
       const int i = it.i0 + g * (f.tile / 2) + row / a.G, hq = it.h * a.G + row % a.G;
@@ -315,77 +360,121 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
       for (int j = it.from[g]; j < it.to[g]; ++j) {
         if (!wait(s_full + 8 * g, n_s++ & 1u)) break;
         tc_after();
-        float s[128];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) tmem_ld(tS + 32 * k, s + 32 * k);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) tmem_ld_wait(s + 32 * k);
-        const int kb = it.key0 + j * kKeys;
-        if (GEN) {
-#pragma unroll
-          for (int k = 0; k < 128; ++k) {
-            float z = s[k] * a.scale;
-            if (a.cap > 0.f) z = a.cap * (1.f - __fdividef(2.f, 1.f + sc::ex2(z * (2.f * kLog2e / a.cap))));
-            z *= kLog2e;
-            if (a.slopes) z -= slope * (float)abs(v.pos - kb - k);
-            s[k] = z;
-          }
-        }
-        if (__any_sync(kFull, v.lo > kb || v.hi < kb + kKeys)) {
-          const int lo = v.lo - kb, hi = v.hi - kb;
-#pragma unroll
-          for (int k = 0; k < 128; ++k)
-            if (k < lo || k >= hi) s[k] = -INFINITY;
-        }
-        float top[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-        for (int k = 4; k < 128; ++k) top[k & 3] = fmaxf(top[k & 3], s[k]);
-        const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
-        if (__any_sync(kFull, mx > m + 8.f)) {
-          const float nm = fmaxf(m, mx), keep = m == -INFINITY ? 0.f : sc::ex2(m - nm);
-          m = nm;
-          l *= keep;
-          if (j > it.from[g]) {                          // the numerator: its last product has ended with this S
-#pragma unroll 1
-            for (int k = 0; k < D; k += 32) {
-              float o[32];
-              tmem_ld(tO + k, o);
-              tmem_ld_wait(o);
-#pragma unroll
-              for (int q = 0; q < 32; ++q) o[q] *= keep;
-              tmem_st(tO + k, reinterpret_cast<const uint32_t*>(o));
-            }
-          }
-        }
-        const float base = m == -INFINITY ? 0.f : m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-        uint32_t p[64];
-#pragma unroll
-        for (int k = 0; k < 64; ++k) {
-          const float p0 = sc::ex2(fmaf(s[2 * k], c, -base)), p1 = sc::ex2(fmaf(s[2 * k + 1], c, -base));
-          sum[k & 1] += p0;
-          sum[2 + (k & 1)] += p1;
-          p[k] = to_pair<T>(p0, p1);
-        }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tmem_st(tS, p);
-        tmem_st(tS + 32, p + 32);
-        tmem_st_wait();
-        if (kb + kKeys > it.r.len && (g == 0 || j < it.from[0] || j >= it.to[0])) {
-          // values behind the last token: zeros (the second half's product follows the first's)
+        const int kb = it.key0 + j * kKeys, lo = v.lo - kb, hi = v.hi - kb;
+        const bool cut = __any_sync(kFull, v.lo > kb || v.hi < kb + kKeys);
+        // values behind the last token become zeros before a product reads them (the second half's follows the first's)
+        auto clear_tail = [&]() {
+          if (kb + kKeys <= it.r.len || (g == 1 && j >= it.from[0] && j < it.to[0])) return true;
           const uint32_t at = n_kv + 2 * j + 1, st = at % NS;
-          if (!wait(kv_full + 8 * st, (at / NS) & 1u)) break;
-          const int r0 = max(0, it.r.len - kb);
-          for (int x = r0 * 8 + row; x < kKeys * 8; x += 128)
+          if (!wait(kv_full + 8 * st, (at / NS) & 1u)) return false;
+          for (int x = max(0, it.r.len - kb) * 8 + row; x < kKeys * 8; x += 128)
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt)
               *reinterpret_cast<uint4*>(smem + C::OFF_KV + st * C::STAGE + kt * C::PANEL + x * 16) =
                   make_uint4(0u, 0u, 0u, 0u);
           sc::fence_proxy_async();
+          return true;
+        };
+        // the running maximum, in base 2, and with it the numerator, whose last product has ended with this S
+        auto raise = [&](float mx) {
+          if (!__any_sync(kFull, mx > m + 8.f)) return;
+          const float nm = fmaxf(m, mx), keep = m == -INFINITY ? 0.f : sc::ex2(m - nm);
+          m = nm;
+          l *= keep;
+          if (j == it.from[g]) return;
+#pragma unroll 1
+          for (int k = 0; k < D; k += 32) {
+            float o[32];
+            tmem_ld(tO + k, o);
+            tmem_ld_wait(o);
+#pragma unroll
+            for (int q = 0; q < 32; ++q) o[q] *= keep;
+            tmem_st(tO + k, reinterpret_cast<const uint32_t*>(o));
+          }
+        };
+        // 32 columns of P to columns [16 k, 16 k + 16) in the place of S; the product may begin with half of them
+        auto weigh = [&](const float* z, int k, float2 mul, float2 sub, float2& sum) {
+          uint32_t p[16];
+#pragma unroll
+          for (int q = 0; q < 16; ++q) {
+            const float2 x = fma2(make_float2(z[2 * q], z[2 * q + 1]), mul, sub);
+            const float2 w = make_float2(sc::ex2(x.x), sc::ex2(x.y));
+            sum = add2(sum, w);
+            p[q] = to_pair<T>(w.x, w.y);
+          }
+          tmem_st16(tS + 16 * k, p);
+        };
+        auto hand_over = [&](int part_of_p) {
+          tmem_st_wait();
+          tc_before();
+          __syncwarp();
+          if (lane == 0) sc::mbar_arrive(p_full + 16 * g + 8 * part_of_p);
+        };
+        float2 sum = make_float2(0.f, 0.f);
+        if constexpr (!GEN) {
+          float s[128];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) tmem_ld(tS + 32 * k, s + 32 * k);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) tmem_ld_wait(s + 32 * k);
+          if (cut) {
+#pragma unroll
+            for (int k = 0; k < 128; ++k)
+              if (k < lo || k >= hi) s[k] = -INFINITY;
+          }
+          raise(top_of<128>(s) * c);
+          const float base = m == -INFINITY ? 0.f : -m;
+          const float2 mul = make_float2(c, c), sub = make_float2(base, base);
+          if (!clear_tail()) break;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            weigh(s + 32 * k, k, mul, sub, sum);
+            if (k & 1) hand_over(k >> 1);
+          }
+        } else {
+          // 32 columns at a time and not unrolled further: the long form would not stay in the instruction cache
+          // (20 us a block instead of 4); the exponents go back to where S was
+          const float ahead = (float)(v.pos - kb);
+          float mx = -INFINITY;
+#pragma unroll 1
+          for (int k = 0; k < 4; ++k) {
+            float z[32];
+            tmem_ld(tS + 32 * k, z);
+            tmem_ld_wait(z);
+            if (a.cap > 0.f) {
+#pragma unroll
+              for (int q = 0; q < 32; ++q) z[q] = fmaf(-2.f * cap2, rcp(1.f + sc::ex2(z[q] * cap_in)), cap2);
+            } else {
+#pragma unroll
+              for (int q = 0; q < 32; ++q) z[q] *= c;
+            }
+            if (a.slopes) {
+              const float d = ahead - (float)(32 * k);
+#pragma unroll
+              for (int q = 0; q < 32; ++q) z[q] = fmaf(-slope, fabsf(d - (float)q), z[q]);
+            }
+            if (cut) {
+#pragma unroll
+              for (int q = 0; q < 32; ++q)
+                if (32 * k + q < lo || 32 * k + q >= hi) z[q] = -INFINITY;
+            }
+            mx = fmaxf(mx, top_of<32>(z));
+            tmem_st(tS + 32 * k, reinterpret_cast<const uint32_t*>(z));
+          }
+          tmem_st_wait();
+          raise(mx);
+          const float base = m == -INFINITY ? 0.f : -m;
+          if (!clear_tail()) break;
+#pragma unroll 1
+          for (int k = 0; k < 4; ++k) {
+            float z[32];
+            tmem_ld(tS + 32 * k, z);
+            tmem_ld_wait(z);
+            weigh(z, k, make_float2(1.f, 1.f), make_float2(base, base), sum);
+            if (k & 1) hand_over(k >> 1);
+          }
         }
-        tc_before();
-        __syncwarp();
-        if (lane == 0) sc::mbar_arrive(p_full + 8 * g);
+        l += sum.x + sum.y;
       }
       if (!ok) break;
       // --- the half's result
@@ -469,16 +558,21 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
               if (j > it.from[g] && j <= it.to[g]) {     // O += P V of block j - 1
-                if (!wait(p_full + 8 * g, n_p[g]++ & 1u)) break;
-                tc_after();
-                if (lane == 0) {
-                  const uint32_t v0 = sb + C::OFF_KV + vs * C::STAGE;
+                const uint32_t v0 = sb + C::OFF_KV + vs * C::STAGE;
 #pragma unroll
-                  for (int k = 0; k < kKeys / 16; ++k)
-                    mma_ts(tmem + 256 + 128 * g, tmem + 128 * g + 8 * k, desc_at(dv, v0 + 2048 * k), id_o,
-                           j - 1 > it.from[g] || k > 0 ? 1u : 0u);
-                  if (j == it.to[g]) commit(o_full + 8 * g);
+                for (int q = 0; q < 2; ++q) {
+                  if (!wait(p_full + 16 * g + 8 * q, n_p[g] & 1u)) break;
+                  tc_after();
+                  if (lane == 0) {
+#pragma unroll
+                    for (int k = q * (kKeys / 32); k < (q + 1) * (kKeys / 32); ++k)
+                      mma_ts(tmem + 256 + 128 * g, tmem + 128 * g + 8 * k, desc_at(dv, v0 + 2048 * k), id_o,
+                             j - 1 > it.from[g] || k > 0 ? 1u : 0u);
+                    if (q == 1 && j == it.to[g]) commit(o_full + 8 * g);
+                  }
                 }
+                if (!ok) break;
+                ++n_p[g];
               }
               if (j >= it.from[g] && j < it.to[g]) {     // S = Q K^T of block j
                 tc_after();
