@@ -69,11 +69,11 @@ struct TilesCfg {
 // of 128 bytes, groups of 8 rows 1024 bytes apart; 16 elements along K are 32
 // bytes.  MN-major (V as [keys][columns]): groups of 8 keys 1024 bytes apart,
 // the next 64 columns a panel further; 16 keys are 2048 bytes.
-__device__ __forceinline__ uint64_t desc_base(int leading, int stride) {
-  return ((uint64_t)(leading >> 4) << 16) | ((uint64_t)(stride >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
-__device__ __forceinline__ uint64_t desc_at(uint64_t base, uint32_t addr) {
-  return base | (uint64_t)((addr >> 4) & 0x3FFFu);
+// A descriptor is a constant high word and a low word that holds the address,
+// so that stepping through an operand is one addition.
+__device__ __forceinline__ uint32_t desc_hi(int stride) { return (uint32_t)(stride >> 4) | (1u << 14) | (2u << 29); }
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, int leading) {
+  return (addr >> 4) | ((uint32_t)(leading >> 4) << 16);
 }
 template <typename T>
 __device__ __forceinline__ uint32_t idesc(int n, bool v_major) {
@@ -81,16 +81,19 @@ __device__ __forceinline__ uint32_t idesc(int n, bool v_major) {
   return (1u << 4) | (f << 7) | (f << 10) | (v_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
          ((uint32_t)(kHalf >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t da, uint64_t db, uint32_t id, uint32_t acc) {
+template <bool ADD>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t id) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(da), "l"(db), "r"(id), "r"(acc)
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %3};\n setp.ne.b32 p, %5, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n}\n" ::"r"(d), "r"(a_lo), "r"(b_lo), "r"(hi), "r"(id),
+      "n"(ADD ? 1 : 0)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t ta, uint64_t db, uint32_t id, uint32_t acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t ta, uint32_t b_lo, uint32_t hi, uint32_t id, uint32_t add) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(ta), "l"(db), "r"(id), "r"(acc)
+      "{\n .reg .pred p;\n .reg .b64 b;\n mov.b64 b, {%2, %3};\n setp.ne.b32 p, %5, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(d), "r"(ta), "r"(b_lo), "r"(hi), "r"(id),
+      "r"(add)
       : "memory");
 }
 __device__ __forceinline__ void commit(uint32_t bar) {
@@ -152,6 +155,18 @@ __device__ __forceinline__ void tma_q(uint32_t dst, const CUtensorMap* tm, int c
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
       "[%5];\n" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tm)), "r"(col), "r"(head), "r"(row), "r"(bar)
       : "memory");
+}
+
+// One look at a barrier's phase, without the suspension that mbar_try asks for
+// (waking from it costs more than the usual wait here).
+__device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 // ---------------------------------------------------------------------------
@@ -332,13 +347,19 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
   }
   Item it;
   bool ok = true;
-  auto wait = [&](uint32_t bar, uint32_t parity) {       // two seconds at most; after one failure at once
-    if (ok && !sc::mbar_try(bar, parity) && !sc::mbar_wait(bar, parity, sc::gtimer() + 2000000000LL)) {
-      ok = false;
-      set_error(a.err, E_TIMEOUT);
-    }
-    ok = __all_sync(kFull, ok);
-    return ok;
+  auto wait_one = [&](uint32_t bar, uint32_t parity) {   // this thread alone; two seconds at most
+    if (poll(bar, parity)) return true;
+    const long long end = sc::gtimer() + 2000000000LL;
+    for (uint32_t n = 1; !poll(bar, parity); ++n)
+      if ((n & 255u) == 0u && sc::gtimer() > end) {
+        set_error(a.err, E_TIMEOUT);
+        return false;
+      }
+    return true;
+  };
+  auto wait = [&](uint32_t bar, uint32_t parity) {       // a warp together; after one failure at once
+    ok = ok && wait_one(bar, parity);
+    return ok = __all_sync(kFull, ok);
   };
 
   if (warp < 8) {
@@ -544,59 +565,68 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRestRegs));
     if (warp == 8) {
       // ================= products (one thread) =================
-      const uint64_t dk = desc_base(16, 1024), dv = desc_base(C::PANEL, 1024);
-      const uint32_t id_s = idesc<T>(kKeys, false), id_o = idesc<T>(D, true);
-      uint32_t n_kv = 0, n_q = 0, n_p[2] = {0, 0};
+      // This thread must not fall behind: the tensor cores' queue is short, and what it spends on waits and addresses
+      // beyond a product's own time they spend idle (with votes of the warp at each wait and descriptors made
+      // anew it took 4000 cycles a block, of which the products are 2048).
+      const uint32_t hi = desc_hi(1024), id_s = idesc<T>(kKeys, false), id_o = idesc<T>(D, true);
+      const uint32_t q_lo = desc_lo(sb + C::OFF_Q, 16), k_lo = desc_lo(sb + C::OFF_KV, 16),
+                     v_lo = desc_lo(sb + C::OFF_KV, C::PANEL);
+      uint32_t n_q = 0, n_p0 = 0, n_p1 = 0;
+      uint32_t ks = 0, kp = 0;                           // stage and phase of the next K; its V is the next tile
       while (ok && next_item(f, walk, it)) {
-        const bool used[2] = {it.to[0] > it.from[0], it.to[1] > it.from[1]};
-        if (used[0] || used[1]) {
-          if (!wait(q_full, n_q++ & 1u)) break;
-          for (int j = 0; j <= it.nb && ok; ++j) {
-            const uint32_t kt = n_kv + 2 * j, ks = kt % NS, vt = kt - 1, vs = vt % NS;   // K of block j, V of block j - 1
-            if (j > 0 && !wait(kv_full + 8 * vs, (vt / NS) & 1u)) break;
-            if (j < it.nb && !wait(kv_full + 8 * ks, (kt / NS) & 1u)) break;
+        if (it.to[0] == it.from[0] && it.to[1] == it.from[1]) continue;
+        if (lane == 0) {
+          const int from0 = it.from[0], to0 = it.to[0], from1 = it.from[1], to1 = it.to[1], nb = it.nb;
+          uint32_t vs = 0, vp = 0;                       // of the V whose products come next
+          auto scores = [&](int g) {                     // S = Q K^T
+            tc_after();
+            const uint32_t q = q_lo + g * (C::STAGE >> 4), k = k_lo + ks * (C::STAGE >> 4);
+            mma_ss<false>(tmem + 128 * g, q, k, hi, id_s);
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              if (j > it.from[g] && j <= it.to[g]) {     // O += P V of block j - 1
-                const uint32_t v0 = sb + C::OFF_KV + vs * C::STAGE;
+            for (int i = 1; i < D / 16; ++i)
+              mma_ss<true>(tmem + 128 * g, q + (i >> 2) * (C::PANEL >> 4) + (i & 3) * 2,
+                           k + (i >> 2) * (C::PANEL >> 4) + (i & 3) * 2, hi, id_s);
+            commit(s_full + 8 * g);
+          };
+          auto output = [&](int g, uint32_t& n, bool first, bool last) {     // O += P V
+            const uint32_t v = v_lo + vs * (C::STAGE >> 4);
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                  if (!wait(p_full + 16 * g + 8 * q, n_p[g] & 1u)) break;
-                  tc_after();
-                  if (lane == 0) {
+            for (int h = 0; h < 2; ++h) {
+              if (!wait_one(p_full + 16 * g + 8 * h, n & 1u)) return false;
+              tc_after();
 #pragma unroll
-                    for (int k = q * (kKeys / 32); k < (q + 1) * (kKeys / 32); ++k)
-                      mma_ts(tmem + 256 + 128 * g, tmem + 128 * g + 8 * k, desc_at(dv, v0 + 2048 * k), id_o,
-                             j - 1 > it.from[g] || k > 0 ? 1u : 0u);
-                    if (q == 1 && j == it.to[g]) commit(o_full + 8 * g);
-                  }
-                }
-                if (!ok) break;
-                ++n_p[g];
-              }
-              if (j >= it.from[g] && j < it.to[g]) {     // S = Q K^T of block j
-                tc_after();
-                if (lane == 0) {
-                  const uint32_t q0 = sb + C::OFF_Q + g * C::STAGE, k0 = sb + C::OFF_KV + ks * C::STAGE;
-#pragma unroll
-                  for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t off = (k >> 2) * C::PANEL + (k & 3) * 32;
-                    mma_ss(tmem + 128 * g, desc_at(dk, q0 + off), desc_at(dk, k0 + off), id_s, k > 0 ? 1u : 0u);
-                  }
-                  commit(s_full + 8 * g);
-                }
-              }
+              for (int i = h * (kKeys / 32); i < (h + 1) * (kKeys / 32); ++i)
+                mma_ts(tmem + 256 + 128 * g, tmem + 128 * g + 8 * i, v + i * (2048 >> 4), hi, id_o, !first || i > 0);
             }
-            if (!ok) break;
-            if (lane == 0) {
-              if (j > 0) commit(kv_empty + 8 * vs);
-              if (j < it.nb) commit(kv_empty + 8 * ks);
-              if (j == it.nb) commit(q_empty);
+            ++n;
+            if (last) commit(o_full + 8 * g);
+            return true;
+          };
+          ok = wait_one(q_full, n_q & 1u);
+          for (int j = 0; j <= nb && ok; ++j) {
+            // a stage is waited for as late and released as early as its products allow
+            if (j > 0 && !(ok = wait_one(kv_full + 8 * vs, vp))) break;
+            if (j > from0 && j <= to0 && !(ok = output(0, n_p0, j - 1 == from0, j == to0))) break;
+            if (j < nb && !(ok = wait_one(kv_full + 8 * ks, kp))) break;
+            if (j >= from0 && j < to0) scores(0);
+            if (j > from1 && j <= to1 && !(ok = output(1, n_p1, j - 1 == from1, j == to1))) break;
+            if (j > 0) commit(kv_empty + 8 * vs);
+            if (j >= from1 && j < to1) scores(1);
+            if (j < nb) {
+              commit(kv_empty + 8 * ks);
+              vs = ks + 1;
+              vp = kp;
+              if (vs == NS) { vs = 0; vp ^= 1u; }
+              ks = vs + 1;
+              kp = vp;
+              if (ks == NS) { ks = 0; kp ^= 1u; }
+            } else {
+              commit(q_empty);
             }
-            __syncwarp();
           }
-          n_kv += 2 * it.nb;
         }
+        ++n_q;
+        ok = __all_sync(kFull, ok);
       }
       if (!ok) {                                         // gave up: products under way end before the memory is freed
         if (lane == 0) commit(drain);
