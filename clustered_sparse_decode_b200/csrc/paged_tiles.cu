@@ -81,23 +81,35 @@ __device__ __forceinline__ uint32_t idesc(int n, bool v_major) {
   return (1u << 4) | (f << 7) | (f << 10) | (v_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
          ((uint32_t)(kHalf >> 4) << 24);
 }
+// Products and commits are issued by the one lane whose `one` is set, inside
+// control flow that the whole warp shares: operands then stay in uniform
+// registers (in a branch of one lane each product cost ten moves into them).
 template <bool ADD>
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t id) {
+__device__ __forceinline__ void mma_ss(uint32_t one, uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t id) {
   asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 a, b;\n mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %3};\n setp.ne.b32 p, %5, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n}\n" ::"r"(d), "r"(a_lo), "r"(b_lo), "r"(hi), "r"(id),
-      "n"(ADD ? 1 : 0)
+      "{\n .reg .pred p, q;\n .reg .b64 a, b;\n mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %3};\n setp.ne.b32 p, %5, 0;\n"
+      " setp.ne.b32 q, %6, 0;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n}\n" ::"r"(d), "r"(a_lo),
+      "r"(b_lo), "r"(hi), "r"(id), "n"(ADD ? 1 : 0), "r"(one)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t ta, uint32_t b_lo, uint32_t hi, uint32_t id, uint32_t add) {
+__device__ __forceinline__ void mma_ts(uint32_t one, uint32_t d, uint32_t ta, uint32_t b_lo, uint32_t hi, uint32_t id,
+                                       uint32_t add) {
   asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 b;\n mov.b64 b, {%2, %3};\n setp.ne.b32 p, %5, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(d), "r"(ta), "r"(b_lo), "r"(hi), "r"(id),
-      "r"(add)
+      "{\n .reg .pred p, q;\n .reg .b64 b;\n mov.b64 b, {%2, %3};\n setp.ne.b32 p, %5, 0;\n setp.ne.b32 q, %6, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(d), "r"(ta), "r"(b_lo), "r"(hi), "r"(id),
+      "r"(add), "r"(one)
       : "memory");
 }
-__device__ __forceinline__ void commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar) : "memory");
+__device__ __forceinline__ void commit(uint32_t one, uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar), "r"(one)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t one;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+  return one;
 }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
@@ -568,68 +580,70 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
       // This thread must not fall behind: the tensor cores' queue is short, and what it spends on waits and addresses
       // beyond a product's own time they spend idle (with votes of the warp at each wait and descriptors made
       // anew it took 4000 cycles a block, of which the products are 2048).
+      const uint32_t one = elect_one();
       const uint32_t hi = desc_hi(1024), id_s = idesc<T>(kKeys, false), id_o = idesc<T>(D, true);
       const uint32_t q_lo = desc_lo(sb + C::OFF_Q, 16), k_lo = desc_lo(sb + C::OFF_KV, 16),
                      v_lo = desc_lo(sb + C::OFF_KV, C::PANEL);
+      const uint32_t acc = __shfl_sync(kFull, tmem, 0);
       uint32_t n_q = 0, n_p0 = 0, n_p1 = 0;
       uint32_t ks = 0, kp = 0;                           // stage and phase of the next K; its V is the next tile
       while (ok && next_item(f, walk, it)) {
         if (it.to[0] == it.from[0] && it.to[1] == it.from[1]) continue;
-        if (lane == 0) {
-          const int from0 = it.from[0], to0 = it.to[0], from1 = it.from[1], to1 = it.to[1], nb = it.nb;
-          uint32_t vs = 0, vp = 0;                       // of the V whose products come next
-          auto scores = [&](int g) {                     // S = Q K^T
+        const int from0 = __shfl_sync(kFull, it.from[0], 0), to0 = __shfl_sync(kFull, it.to[0], 0),
+                  from1 = __shfl_sync(kFull, it.from[1], 0), to1 = __shfl_sync(kFull, it.to[1], 0),
+                  nb = __shfl_sync(kFull, it.nb, 0);
+        uint32_t vs = 0, vp = 0;                         // of the V whose products come next
+        auto scores = [&](uint32_t g) {                  // S = Q K^T
+          tc_after();
+          const uint32_t q = q_lo + g * (C::STAGE >> 4), k = k_lo + ks * (C::STAGE >> 4);
+          mma_ss<false>(one, acc + 128 * g, q, k, hi, id_s);
+#pragma unroll
+          for (int i = 1; i < D / 16; ++i)
+            mma_ss<true>(one, acc + 128 * g, q + (i >> 2) * (C::PANEL >> 4) + (i & 3) * 2,
+                         k + (i >> 2) * (C::PANEL >> 4) + (i & 3) * 2, hi, id_s);
+          commit(one, s_full + 8 * g);
+        };
+        auto output = [&](uint32_t g, uint32_t& n, bool first, bool last) {  // O += P V
+          const uint32_t v = v_lo + vs * (C::STAGE >> 4);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (!wait_one(p_full + 16 * g + 8 * h, n & 1u)) return false;
             tc_after();
-            const uint32_t q = q_lo + g * (C::STAGE >> 4), k = k_lo + ks * (C::STAGE >> 4);
-            mma_ss<false>(tmem + 128 * g, q, k, hi, id_s);
 #pragma unroll
-            for (int i = 1; i < D / 16; ++i)
-              mma_ss<true>(tmem + 128 * g, q + (i >> 2) * (C::PANEL >> 4) + (i & 3) * 2,
-                           k + (i >> 2) * (C::PANEL >> 4) + (i & 3) * 2, hi, id_s);
-            commit(s_full + 8 * g);
-          };
-          auto output = [&](int g, uint32_t& n, bool first, bool last) {     // O += P V
-            const uint32_t v = v_lo + vs * (C::STAGE >> 4);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if (!wait_one(p_full + 16 * g + 8 * h, n & 1u)) return false;
-              tc_after();
-#pragma unroll
-              for (int i = h * (kKeys / 32); i < (h + 1) * (kKeys / 32); ++i)
-                mma_ts(tmem + 256 + 128 * g, tmem + 128 * g + 8 * i, v + i * (2048 >> 4), hi, id_o, !first || i > 0);
-            }
-            ++n;
-            if (last) commit(o_full + 8 * g);
-            return true;
-          };
-          ok = wait_one(q_full, n_q & 1u);
-          for (int j = 0; j <= nb && ok; ++j) {
-            // a stage is waited for as late and released as early as its products allow
-            if (j > 0 && !(ok = wait_one(kv_full + 8 * vs, vp))) break;
-            if (j > from0 && j <= to0 && !(ok = output(0, n_p0, j - 1 == from0, j == to0))) break;
-            if (j < nb && !(ok = wait_one(kv_full + 8 * ks, kp))) break;
-            if (j >= from0 && j < to0) scores(0);
-            if (j > from1 && j <= to1 && !(ok = output(1, n_p1, j - 1 == from1, j == to1))) break;
-            if (j > 0) commit(kv_empty + 8 * vs);
-            if (j >= from1 && j < to1) scores(1);
-            if (j < nb) {
-              commit(kv_empty + 8 * ks);
-              vs = ks + 1;
-              vp = kp;
-              if (vs == NS) { vs = 0; vp ^= 1u; }
-              ks = vs + 1;
-              kp = vp;
-              if (ks == NS) { ks = 0; kp ^= 1u; }
-            } else {
-              commit(q_empty);
-            }
+            for (int i = h * (kKeys / 32); i < (h + 1) * (kKeys / 32); ++i)
+              mma_ts(one, acc + 256 + 128 * g, acc + 128 * g + 8 * i, v + i * (2048 >> 4), hi, id_o, !first || i > 0);
+          }
+          ++n;
+          if (last) commit(one, o_full + 8 * g);
+          return true;
+        };
+        ok = wait_one(q_full, n_q & 1u);
+        for (int j = 0; j <= nb && ok; ++j) {
+          // a stage is waited for as late and released as early as its products allow
+          if (j > 0 && !(ok = wait_one(kv_full + 8 * vs, vp))) break;
+          if (j > from0 && j <= to0 && !(ok = output(0, n_p0, j - 1 == from0, j == to0))) break;
+          if (j < nb && !(ok = wait_one(kv_full + 8 * ks, kp))) break;
+          if (j >= from0 && j < to0) scores(0);
+          if (j > from1 && j <= to1 && !(ok = output(1, n_p1, j - 1 == from1, j == to1))) break;
+          if (j > 0) commit(one, kv_empty + 8 * vs);
+          if (j >= from1 && j < to1) scores(1);
+          if (j < nb) {
+            commit(one, kv_empty + 8 * ks);
+            vs = ks + 1;
+            vp = kp;
+            if (vs == NS) { vs = 0; vp ^= 1u; }
+            ks = vs + 1;
+            kp = vp;
+            if (ks == NS) { ks = 0; kp ^= 1u; }
+          } else {
+            commit(one, q_empty);
           }
         }
         ++n_q;
         ok = __all_sync(kFull, ok);
       }
       if (!ok) {                                         // gave up: products under way end before the memory is freed
-        if (lane == 0) commit(drain);
+        commit(one, drain);
         sc::mbar_wait(drain, 0, sc::gtimer() + 200000000LL);
       }
     } else if (warp == 9) {
