@@ -13,7 +13,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libmpattn.so")
 SOURCES = ["api.cu", "assign_tc.cu", "decode.cu", "decode_static.cu", "decode_unit.cu", "kmeans.cu", "paged.cu",
-           "paged_attend.cu", "paged_rows.cu", "paged_tiles.cu",
+           "paged_attend.cu", "paged_f32.cu", "paged_rows.cu", "paged_tiles.cu",
            "paged_work.cu"]
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
               "-Xcompiler", "-fPIC", "--shared", "--threads", "0"]

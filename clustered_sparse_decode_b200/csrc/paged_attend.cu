@@ -1,43 +1,11 @@
-// Attention of new tokens over a paged cache: the choice of kernel, its scratch,
-// and the row-by-row kernel.
+// Attention of new tokens over a paged cache: the choice of kernel and its
+// scratch.
 #include <algorithm>
 
 #include "paged_work.cuh"
 
 namespace mp {
 namespace paged {
-
-// One warp a (row, query head): the operator as its definition reads.
-constexpr int kRowWarps = 8;
-
-template <typename T, int D>
-__global__ void __launch_bounds__(kRowWarps * 32) rows_plain(const Attend a) {
-  const int Hq = a.H * a.G, lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
-  // every request's offsets and length are looked at, those without rows too
-  for (int64_t b = w; b < a.batch; b += (int64_t)gridDim.x * kRowWarps)
-    if (lane == 0) request_of(a, (int)b);
-  if (w >= (int64_t)a.rows * Hq) return;
-  const int t = (int)(w / Hq), hq = (int)(w % Hq);
-  if (t >= min(__ldg(a.cu + a.batch), a.rows)) return;
-  int lo = 0, hi = a.batch;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(a.cu + mid) <= t) lo = mid;
-    else hi = mid;
-  }
-  const Request r = request_of(a, lo);
-  const int i = t - r.row0;
-  if (i < 0 || i >= r.n) return;
-  RowState<T, D> s;
-  attend_row<T, D>(a, lo, r, i, hq, 0, r.len, s);
-  T* o = reinterpret_cast<T*>(a.O + (int64_t)t * a.o_row_b + (int64_t)hq * a.o_head_b) + lane * (D / 32);
-  const bool none = s.l == 0.f;
-  const float inv = none ? 0.f : 1.f / s.l;
-#pragma unroll
-  for (int e = 0; e < D / 32; ++e) o[e] = from_f32<T>(s.acc[e] * inv);
-  if (a.lse && lane == 0) a.lse[(int64_t)t * Hq + hq] = none ? -INFINITY : (s.m + log2f(s.l)) / kLog2e;
-}
 
 static int log2_of(int x) {
   int s = 0;
@@ -84,52 +52,49 @@ static Attend args_of(const mp_paged_cache& c, const mp_paged_attend_args& p) {
   return a;
 }
 
-template <typename T>
-static void launch_plain(const Attend& a, int D, cudaStream_t st) {
-  const unsigned grid = (unsigned)(((int64_t)a.rows * a.H * a.G + kRowWarps - 1) / kRowWarps);
-  if (D == 128) rows_plain<T, 128><<<grid, kRowWarps * 32, 0, st>>>(a);
-  else rows_plain<T, 64><<<grid, kRowWarps * 32, 0, st>>>(a);
-}
-
-// How a call is done.  Few (token, head) rows a KV head: paged_rows.cu, blocks
-// in clusters of one unit (one launch) while a block's part of the longest
-// request that the table can hold stays short, shares over all SMs otherwise
-// (two or three launches, the same time whatever the lengths).  More rows:
-// paged_tiles.cu.  fp32: row by row.
+// How a call is done.  16-bit types with few (token, head) rows a KV head:
+// paged_rows.cu; with more: paged_tiles.cu; fp32: paged_f32.cu.  The first and the
+// last run as clusters of one unit (one launch, no scratch) while a block's part
+// of the longest request that the table can hold stays short, otherwise with
+// shares over all SMs (two or three launches, the same time whatever the
+// lengths).
 constexpr int kFewCells = 32;          // rows that the few-rows kernel takes
-constexpr int kFewParts = kMostParts;  // two blocks an SM
-constexpr int kTilesParts = 148;       // one
+constexpr int kSMs = 148;
 constexpr int kClusterBlocks = 16;     // blocks of keys of a clustered block at most
 
 struct Way {
-  bool few, tiles;
-  int cells, cluster, entries, rows, parts;
+  enum { FEW, TILES, F32 } kind;
+  int cells, cluster, entries, rows, tile, parts, least;
 };
 
 static Way way_of(const mp_paged_cache& c, const mp_paged_attend_args& p) {
   Way w{};
   const int G = p.q_heads / c.cfg.kv_heads, max_new = p.max_new ? p.max_new : p.rows;
-  if (c.cfg.dtype == MP_F32) return w;
-  if ((int64_t)max_new * G > kFewCells) {
-    w.tiles = true;
-    w.entries = p.rows / tiles_tokens(G) + p.batch;
+  const int64_t cells = (int64_t)max_new * G;
+  w.least = 4;
+  if (c.cfg.dtype != MP_F32 && cells > kFewCells) {
+    w.kind = Way::TILES;
     w.rows = kTilesRows;
-    w.parts = kTilesParts;
-    return w;
+    w.tile = tiles_tokens(G);
+    w.parts = kSMs;                    // one block an SM
+  } else {
+    const bool f32 = c.cfg.dtype == MP_F32;
+    w.kind = f32 ? Way::F32 : Way::FEW;
+    w.cells = (int)(cells < 32 ? cells : 32);
+    w.rows = f32 ? f32_rows(w.cells) : few_rows(w.cells);
+    w.tile = f32 ? w.rows / G : max_new;
+    const int blocks_sm = f32 ? 1 : 2;
+    const int64_t units = (int64_t)p.batch * c.cfg.kv_heads * ((max_new + w.tile - 1) / w.tile);
+    const int64_t blocks = ((int64_t)p.table_pages * c.cfg.page_tokens + kFewBlock - 1) / kFewBlock;
+    int k = 1;
+    while (k < 8 && units * k < blocks_sm * kSMs) k *= 2;
+    if (blocks <= (int64_t)kClusterBlocks * k && units * k <= (1 << 30)) {
+      w.cluster = k;
+      return w;
+    }
+    w.parts = blocks_sm * kSMs;
   }
-  w.few = true;
-  w.cells = max_new * G;
-  const int64_t units = (int64_t)p.batch * c.cfg.kv_heads;
-  const int64_t blocks = ((int64_t)p.table_pages * c.cfg.page_tokens + kFewBlock - 1) / kFewBlock;
-  int k = 1;
-  while (k < 8 && units * k < kFewParts) k *= 2;
-  if (blocks <= (int64_t)kClusterBlocks * k && units * k <= (1 << 30)) {
-    w.cluster = k;
-    return w;
-  }
-  w.entries = p.rows / max_new + p.batch;
-  w.rows = few_rows(w.cells);
-  w.parts = kFewParts;
+  w.entries = p.rows / w.tile + p.batch;
   return w;
 }
 
@@ -167,18 +132,13 @@ mp_status paged_attend_impl(const mp_paged_cache& c, const mp_paged_attend_args&
                             cudaStream_t st) {
   const paged::Attend a = paged::args_of(c, p);
   const paged::Way w = paged::way_of(c, p);
-  cudaError_t e = cudaSuccess;
+  cudaError_t e;
   paged::Work work{};
   paged::lay_work(w, c.cfg.head_dim, scratch, &work);
-  if (w.few) {
-    work.least = 4;
-    e = paged::attend_few(a, c, work, w.cells, w.cluster, st);
-  } else if (w.tiles) {
-    work.least = 4;
-    e = paged::attend_tiles(a, c, work, w.entries, st);
-  } else {
-    paged::launch_plain<float>(a, c.cfg.head_dim, st);
-  }
+  work.least = w.least;
+  if (w.kind == paged::Way::FEW) e = paged::attend_few(a, c, work, w.cells, w.cluster, st);
+  else if (w.kind == paged::Way::TILES) e = paged::attend_tiles(a, c, work, st);
+  else e = paged::attend_f32(a, c, work, w.rows, w.tile, w.cluster, st);
   if (e == cudaSuccess) return cudaGetLastError() == cudaSuccess ? MP_OK : MP_ECUDA;
   cudaGetLastError();
   return e == cudaErrorNotSupported ? MP_EUNSUPPORTED : MP_ECUDA;

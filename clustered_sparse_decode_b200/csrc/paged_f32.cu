@@ -1,0 +1,309 @@
+// Attention over a paged cache in fp32, any number of rows.
+//
+// fp32 products have no fast matrix instruction that keeps their precision, so
+// both products run on the ordinary multiply-add units.  A block's 4 warps take
+// every fourth 16-key tile of its share; each streams its tiles through its own
+// ring of shared-memory stages with cp.async (rows behind the last token are
+// filled with zeros).  Scores: lane l computes key l % 16 against half of the
+// tile's rows (4, 8 or 16 (token, head) rows in all), keys from rows padded by 16
+// bytes so that 8 lanes' vector loads fall into different banks, queries
+// broadcast.  Output: lane l owns columns [l D/32, (l + 1) D/32) of all rows, the
+// weights come back from shared memory.  Single tokens are bound by reading the
+// cache once; 16 rows by the multiply-adds and their shared-memory reads (one
+// vector read a 4 multiply-adds a lane).
+#include "paged_work.cuh"
+#include "stream_common.cuh"
+
+namespace mp {
+namespace paged {
+
+constexpr int kF32Warps = 4;
+constexpr int kF32Tile = 16;                       // keys a tile
+static_assert(kFewBlock == kF32Warps * kF32Tile, "a block of the share-out is a tile a warp");
+
+struct F32 {
+  Attend a;
+  Work w;
+  int tile;                                        // tokens a tile
+  int cluster;                                     // > 0: that many blocks share a unit
+};
+
+template <int D, int RH>                           // RH rows a half warp
+struct F32Cfg {
+  static constexpr int ROWS = 2 * RH;
+  static constexpr int KP = D + 4;                                    // floats between rows of keys
+  static constexpr int STAGE = kF32Tile * (KP + D) * 4;
+  static constexpr int NS = 3;
+  static constexpr int WARP = NS * STAGE + kF32Tile * ROWS * 4;       // ring and weights
+  static constexpr int PITCH = D + 8;
+  static constexpr int OFF_Q = kF32Warps * WARP;                      // [ROWS][D]
+  static constexpr int OFF_ML = OFF_Q + ROWS * D * 4;
+  static constexpr int OFF_UNIT = OFF_ML + kF32Warps * 2 * ROWS * 4;
+  static constexpr int OFF_BAD = OFF_UNIT + 2 * ROWS * 4;
+  static constexpr int SMEM = OFF_BAD + ROWS * 4;
+  static_assert(ROWS * PITCH * 4 <= NS * STAGE, "a warp's numerators fit its ring");
+  static_assert(SMEM <= 227 * 1024 && WARP % 16 == 0 && STAGE % 16 == 0, "shared memory");
+};
+
+template <int D, int RH>
+__global__ void __launch_bounds__(kF32Warps * 32) f32_kernel(const F32 f) {
+  using C = F32Cfg<D, RH>;
+  constexpr int ROWS = C::ROWS, NS = C::NS, E = D / 32;
+  const Attend& a = f.a;
+  extern __shared__ __align__(16) unsigned char smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, half = lane >> 4, key = lane & 15;
+  float* ring = reinterpret_cast<float*>(smem + warp * C::WARP);
+  float* pw = reinterpret_cast<float*>(smem + warp * C::WARP + NS * C::STAGE);     // [16 keys][ROWS]
+  float* q = reinterpret_cast<float*>(smem + C::OFF_Q);
+  float* ml = reinterpret_cast<float*>(smem + C::OFF_ML);
+  const uint32_t ring_s = sc::smem_u32(ring);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  int64_t W = 0, x = 0, x1 = 1;
+  int E0 = 0, N = 1, e = 0;
+  const int part = f.cluster ? (int)(blockIdx.x % f.cluster) : (int)blockIdx.x;
+  if (!f.cluster) {
+    E0 = f.w.count[0];
+    W = E0 > 0 ? f.w.before[E0] * a.H : 0;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (W == 0) return;
+    N = parts_used(f.w, W);
+    if (part >= N) return;
+    x = share(W, N, part);
+    x1 = share(W, N, part + 1);
+    if (x >= x1) return;
+    e = entry_of_warp(f.w.before, E0, a.H, x);
+  }
+  const int64_t start = x;
+
+  while (x < x1) {
+    Settle st;
+    int blk0, blk1, k0;
+    int64_t u0 = 0, u1 = 1;
+    Entry en;
+    if (f.cluster) {
+      const int u = blockIdx.x / f.cluster, tiles = (a.max_new + f.tile - 1) / f.tile;
+      en.tile = u % tiles;
+      st.h = u / tiles % a.H;
+      en.b = u / tiles / a.H;
+    } else {
+      while (f.w.before[e + 1] * a.H <= x) ++e;
+      const int64_t n = f.w.before[e + 1] - f.w.before[e], first = f.w.before[e] * a.H;
+      en = f.w.entry[e];
+      st.h = (int)((x - first) / n);
+      u0 = first + st.h * n;
+      u1 = u0 + n;
+    }
+    st.b = en.b;
+    st.r = request_of(a, en.b);
+    st.i0 = en.tile * f.tile;
+    st.cells = max(0, min(st.r.n - st.i0, f.tile)) * a.G;
+    const int prefix = prefix_of(a, en.b);
+    if (f.cluster) span_of(a, st.r, en.b, st.i0, min(st.r.n, st.i0 + f.tile), kFewBlock, en);
+    k0 = en.k0;
+    blk0 = f.cluster ? (int)((int64_t)en.n * part / f.cluster) : (int)(x - u0);
+    blk1 = f.cluster ? (int)((int64_t)en.n * (part + 1) / f.cluster) : (int)(min(x1, u1) - u0);
+    // this lane's rows
+    int lo[RH], hi[RH], pos[RH], top = 0;
+    float slope[RH];
+#pragma unroll
+    for (int k = 0; k < RH; ++k) {
+      const int row = half * RH + k;
+      lo[k] = 0;
+      hi[k] = 0;
+      pos[k] = 0;
+      slope[k] = 0.f;
+      if (row >= st.cells) continue;
+      const Interval v = interval_of(a, st.r, prefix, st.i0 + row / a.G);
+      lo[k] = v.lo;
+      hi[k] = v.hi;
+      pos[k] = v.pos;
+      if (a.slopes) slope[k] = __ldg(a.slopes + st.h * a.G + row % a.G);
+      if (v.hi > v.lo) top = max(top, v.hi);
+    }
+    top = __reduce_max_sync(kFull, top);
+    st.key0 = k0 + blk0 * kFewBlock;
+    st.key1 = min(k0 + blk1 * kFewBlock, top);
+    for (int c = tid; c < ROWS * D / 4; c += kF32Warps * 32) {
+      const int row = c / (D / 4), d = c % (D / 4);
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (row < st.cells)
+        v = *reinterpret_cast<const float4*>(a.Q + (int64_t)(st.r.row0 + st.i0 + row / a.G) * a.q_row_b +
+                                             (int64_t)(st.h * a.G + row % a.G) * a.q_head_b + d * 16);
+      reinterpret_cast<float4*>(q)[c] = v;
+    }
+    __syncthreads();
+
+    // --- this warp's tiles: keys key0 + 16 (warp + 4 i)
+    const int first = st.key0 + warp * kF32Tile;
+    const int tiles = st.key1 > first ? (st.key1 - first + kFewBlock - 1) / kFewBlock : 0;
+    int pages = -1;                    // lane l: the page of tile 32 (i / 32) + l
+    uint32_t void_stages = 0;
+    auto fetch = [&](int i) {          // always one group, empty behind the last tile
+      if (i < tiles) {
+        if ((i & 31) == 0) pages = i + lane < tiles ? page_of(a, en.b, first + (i + lane) * kFewBlock) : -1;
+        const int page = __shfl_sync(kFull, pages, i & 31), j = first + i * kFewBlock, s = i % NS;
+        void_stages = page < 0 ? void_stages | 1u << s : void_stages & ~(1u << s);
+        if (page >= 0) {
+          const int64_t off = page * a.page_b + st.h * a.head_b + (j & ((1 << a.page_shift) - 1)) * a.tok_b;
+#pragma unroll 4
+          for (int c = lane; c < kF32Tile * D / 4; c += 32) {
+            const int row = c / (D / 4), d = c % (D / 4);
+            const bool in = j + row < st.r.len;
+            const int64_t at = off + (in ? row * a.tok_b : 0) + d * 16;
+            sc::cp16(ring_s + s * C::STAGE + (row * C::KP + d * 4) * 4, a.K + at, in);
+            sc::cp16(ring_s + s * C::STAGE + (kF32Tile * C::KP + row * D + d * 4) * 4, a.V + at, in);
+          }
+        }
+      }
+      sc::cp_commit();
+    };
+    float acc[ROWS][E], m[RH], l[RH];
+#pragma unroll
+    for (int k = 0; k < RH; ++k) { m[k] = -INFINITY; l[k] = 0.f; }
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+      for (int c = 0; c < E; ++c) acc[r][c] = 0.f;
+    for (int i = 0; i < NS - 1; ++i) fetch(i);
+    for (int i = 0; i < tiles; ++i) {
+      fetch(i + NS - 1);
+      asm volatile("cp.async.wait_group %0;\n" ::"n"(NS - 1) : "memory");
+      __syncwarp();
+      const int s = i % NS, j = first + i * kFewBlock + key;
+      if (!(void_stages >> s & 1u)) {
+        const float* kr = ring + s * (C::STAGE / 4) + key * C::KP;
+        const float* vr = ring + s * (C::STAGE / 4) + kF32Tile * C::KP + lane * E;
+        float z[RH];
+#pragma unroll
+        for (int k = 0; k < RH; ++k) z[k] = 0.f;
+#pragma unroll 8
+        for (int d = 0; d < D; d += 4) {
+          const float4 kv = *reinterpret_cast<const float4*>(kr + d);
+#pragma unroll
+          for (int k = 0; k < RH; ++k) {
+            const float4 qv = *reinterpret_cast<const float4*>(q + (half * RH + k) * D + d);
+            z[k] = fmaf(qv.x, kv.x, fmaf(qv.y, kv.y, fmaf(qv.z, kv.z, fmaf(qv.w, kv.w, z[k]))));
+          }
+        }
+        bool grow = false;
+#pragma unroll
+        for (int k = 0; k < RH; ++k) {
+          z[k] = j < lo[k] || j >= hi[k] ? -INFINITY : score2(a, z[k], slope[k], pos[k] - j);
+          grow |= z[k] > m[k] + 8.f;
+        }
+        if (__any_sync(kFull, grow)) {
+          float keep[RH];
+#pragma unroll
+          for (int k = 0; k < RH; ++k) {
+            float t = z[k];
+#pragma unroll
+            for (int o = 8; o; o >>= 1) t = fmaxf(t, __shfl_xor_sync(kFull, t, o));
+            const float nm = fmaxf(m[k], t);
+            keep[k] = m[k] == -INFINITY ? 0.f : exp2f(m[k] - nm);
+            m[k] = nm;
+            l[k] *= keep[k];
+          }
+#pragma unroll
+          for (int r = 0; r < ROWS; ++r) {
+            const float kp = __shfl_sync(kFull, keep[r % RH], r < RH ? 0 : 16);
+#pragma unroll
+            for (int c = 0; c < E; ++c) acc[r][c] *= kp;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < RH; ++k) {
+          const float p = exp2f(z[k] - (m[k] == -INFINITY ? 0.f : m[k]));
+          l[k] += p;
+          pw[key * ROWS + half * RH + k] = p;
+        }
+        __syncwarp();
+#pragma unroll 4
+        for (int t = 0; t < kF32Tile; ++t) {
+          float v[E], p[ROWS];
+#pragma unroll
+          for (int c = 0; c < E; c += 2) *reinterpret_cast<float2*>(v + c) = *reinterpret_cast<const float2*>(vr + t * D + c);
+#pragma unroll
+          for (int r = 0; r < ROWS; r += 4) *reinterpret_cast<float4*>(p + r) = *reinterpret_cast<const float4*>(pw + t * ROWS + r);
+#pragma unroll
+          for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+            for (int c = 0; c < E; ++c) acc[r][c] = fmaf(p[r], v[c], acc[r][c]);
+        }
+      }
+      __syncwarp();                    // all lanes have read the stage and the weights
+    }
+    asm volatile("cp.async.wait_group 0;\n" ::: "memory");
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < RH; ++k) {
+      float s = l[k];
+#pragma unroll
+      for (int o = 8; o; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
+      if (key == 0) {
+        const int row = half * RH + k;
+        ml[(warp * 2) * ROWS + row] = s != s ? s : m[k];
+        ml[(warp * 2 + 1) * ROWS + row] = s;
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+      for (int c = 0; c < E; ++c) ring[r * C::PITCH + lane * E + c] = acc[r][c];
+    st.cluster = f.cluster;
+    st.part = part;
+    st.whole = !f.cluster && x == u0 && min(x1, u1) == u1;
+    st.slot = f.cluster ? nullptr : f.w.part + (2 * (int64_t)part + (x == start ? 0 : 1)) * (int64_t)ROWS * (2 + D);
+    settle<float, D, ROWS, C::PITCH, kF32Warps>(a, st, ml, reinterpret_cast<float*>(smem), C::WARP / 4,
+                                                reinterpret_cast<float*>(smem + C::OFF_UNIT),
+                                                reinterpret_cast<int*>(smem + C::OFF_BAD));
+    if (f.cluster) return;
+    __syncthreads();
+    x = min(x1, u1);
+  }
+}
+
+template <int D, int RH>
+static cudaError_t launch_f32_t(const F32& f, int units, cudaStream_t st) {
+  using C = F32Cfg<D, RH>;
+  auto kern = f32_kernel<D, RH>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(f.cluster ? units * f.cluster : f.w.parts));
+  cfg.blockDim = dim3(kF32Warps * 32);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  if (f.cluster) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = f.cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  } else {                             // the list kernel lies before it
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, f);
+}
+
+template <int D>
+static cudaError_t launch_f32(const F32& f, int rows, int units, cudaStream_t st) {
+  if (rows == 4) return launch_f32_t<D, 2>(f, units, st);
+  if (rows == 8) return launch_f32_t<D, 4>(f, units, st);
+  return launch_f32_t<D, 8>(f, units, st);
+}
+
+cudaError_t attend_f32(const Attend& a, const mp_paged_cache& c, const Work& w, int rows, int tile, int cluster,
+                       cudaStream_t st) {
+  F32 f{a, w, tile, cluster};
+  const int D = c.cfg.head_dim, units = cluster ? a.batch * a.H * ((a.max_new + tile - 1) / tile) : 0;
+  cudaError_t e = cluster ? cudaSuccess : launch_work(a, w, tile, kFewBlock, st);
+  if (e == cudaSuccess) e = D == 128 ? launch_f32<128>(f, rows, units, st) : launch_f32<64>(f, rows, units, st);
+  if (e != cudaSuccess || cluster) return e;
+  return launch_join(a, w, MP_F32, D, tile, rows, st);
+}
+
+}  // namespace paged
+}  // namespace mp

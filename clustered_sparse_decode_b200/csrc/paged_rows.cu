@@ -18,15 +18,11 @@
 // type.  The running maximum is lazy: it moves when a score exceeds it by more
 // than 8 (base 2), so weights stay below 256 and the numerator is rarely
 // rescaled.  Statistics and numerators are fp32.
-#include <cooperative_groups.h>
-
 #include <cstring>
 #include <type_traits>
 
 #include "paged_work.cuh"
 #include "stream_common.cuh"
-
-namespace cg = cooperative_groups;
 
 namespace mp {
 namespace paged {
@@ -119,9 +115,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) few_kernel(const __grid_con
   float* num = reinterpret_cast<float*>(smem + warp * kRing);         // this warp's numerators, at a share's end
   float* ml = reinterpret_cast<float*>(smem + C::OFF_ML);
   float* unit_m = reinterpret_cast<float*>(smem + C::OFF_UNIT);
-  float* unit_l = unit_m + ROWS;
   int* bad = reinterpret_cast<int*>(smem + C::OFF_BAD);
-  float* unit_acc = reinterpret_cast<float*>(smem);                   // the block's numerators take warp 0's place
 
   if (lane == 0)
     for (int s = 0; s < NS; ++s) sc::mbar_init(bars + 8 * s, 1);
@@ -448,70 +442,20 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) few_kernel(const __grid_con
           *reinterpret_cast<float2*>(num + row * C::PITCH + nt * 8 + 2 * t4) = v;
         }
       }
-    if (tid < ROWS) bad[tid] = 0;
-    __syncthreads();
-    const int col = tid % D, rows_at_once = kFewWarps * 32 / D;
-    const bool whole_unit = !f.cluster && x == u0 && min(x1, u1) == u1;
-    float* slot = f.cluster ? nullptr
-                            : f.w.part + (2 * (int64_t)part + (x == start ? 0 : 1)) * (int64_t)ROWS * (2 + D);
-    const int64_t Hq = (int64_t)a.H * a.G;
-    // one (row, column) of the block's result: final, a partial in the scratch, or kept for the cluster
-    auto put = [&](int row, int c, float mm, float ll, float v) {
-      if (f.cluster) {
-        unit_acc[row * C::PITCH + c] = v;
-        if (c == 0) { unit_m[row] = mm; unit_l[row] = ll; }
-      } else if (whole_unit) {
-        const bool none = ll == 0.f;
-        const int64_t t = r.row0 + row / a.G, hq = h * a.G + row % a.G;
-        reinterpret_cast<T*>(a.O + t * a.o_row_b + hq * a.o_head_b)[c] = from_f32<T>(none ? 0.f : v / ll);
-        if (a.lse && c == 0) a.lse[t * Hq + hq] = none ? -INFINITY : (mm + log2f(ll)) / kLog2e;
-      } else {
-        slot[2 * ROWS + row * D + c] = v;
-        if (c == 0) { slot[row] = mm; slot[ROWS + row] = ll; }
-      }
-    };
-    for (int row = tid / D; row < min(cells, ROWS); row += rows_at_once) {
-      float mm = -INFINITY, ll = 0.f, v = 0.f;
-#pragma unroll
-      for (int w = 0; w < kFewWarps; ++w) mm = fmaxf(mm, ml[(w * 2) * ROWS + row]);
-#pragma unroll
-      for (int w = 0; w < kFewWarps; ++w) {
-        const float mw = ml[(w * 2) * ROWS + row], k = mw == -INFINITY ? 0.f : sc::ex2(mw - mm);
-        ll = fmaf(k, ml[(w * 2 + 1) * ROWS + row], ll);
-        v = fmaf(k, reinterpret_cast<float*>(smem + w * kRing)[row * C::PITCH + col], v);
-      }
-      // a key that the row does not see can reach its numerator as 0 * (infinity or NaN), and only so
-      if (!isfinite(v) || !isfinite(ll)) bad[row] = 1;
-      put(row, col, mm, ll, v);        // (in a cluster warp 0's numerators are replaced, each by the thread that read it)
-    }
-    __syncthreads();
-    for (int row = warp; row < min(cells, ROWS); row += kFewWarps)
-      if (bad[row]) {
-        RowState<T, D> s;
-        attend_row<T, D>(a, b, r, row / a.G, h * a.G + row % a.G, key0, key1, s);
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) put(row, lane * (D / 32) + i, s.m, s.l, s.acc[i]);
-      }
-    if (f.cluster) {
-      cg::cluster_group cl = cg::this_cluster();
-      cl.sync();
-      for (int cell = part * (kFewWarps * 32) + tid; cell < min(cells, ROWS) * D; cell += f.cluster * kFewWarps * 32) {
-        const int row = cell / D, c = cell % D;
-        float mm = -INFINITY, ll = 0.f, v = 0.f;
-        for (int p = 0; p < f.cluster; ++p) mm = fmaxf(mm, cl.map_shared_rank(unit_m, p)[row]);
-        for (int p = 0; p < f.cluster; ++p) {
-          const float mp = cl.map_shared_rank(unit_m, p)[row], k = mp == -INFINITY ? 0.f : sc::ex2(mp - mm);
-          ll = fmaf(k, cl.map_shared_rank(unit_l, p)[row], ll);
-          if (k != 0.f) v = fmaf(k, cl.map_shared_rank(unit_acc, p)[row * C::PITCH + c], v);
-        }
-        const bool none = ll == 0.f;
-        const int64_t t = r.row0 + row / a.G, hq = h * a.G + row % a.G;
-        reinterpret_cast<T*>(a.O + t * a.o_row_b + hq * a.o_head_b)[c] = from_f32<T>(none ? 0.f : v / ll);
-        if (a.lse && c == 0) a.lse[t * Hq + hq] = none ? -INFINITY : (mm + log2f(ll)) / kLog2e;
-      }
-      cl.sync();                       // no block leaves while its state is read
-      return;
-    }
+    Settle st;
+    st.b = b;
+    st.h = h;
+    st.r = r;
+    st.i0 = 0;
+    st.cells = min(cells, ROWS);
+    st.key0 = key0;
+    st.key1 = key1;
+    st.cluster = f.cluster;
+    st.part = part;
+    st.whole = !f.cluster && x == u0 && min(x1, u1) == u1;
+    st.slot = f.cluster ? nullptr : f.w.part + (2 * (int64_t)part + (x == start ? 0 : 1)) * (int64_t)ROWS * (2 + D);
+    settle<T, D, ROWS, C::PITCH, kFewWarps>(a, st, ml, reinterpret_cast<float*>(smem), kRing / 4, unit_m, bad);
+    if (f.cluster) return;
     sc::fence_proxy_async();           // the numerators were written where the next loads go
     __syncthreads();
     x = min(x1, u1);

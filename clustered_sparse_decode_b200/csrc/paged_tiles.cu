@@ -780,7 +780,7 @@ static bool encode_q(CUtensorMap* tm, const Attend& a, int dtype, int D) {
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-cudaError_t attend_tiles(const Attend& a, const mp_paged_cache& c, const Work& w, int entries, cudaStream_t st) {
+cudaError_t attend_tiles(const Attend& a, const mp_paged_cache& c, const Work& w, cudaStream_t st) {
   Tiles f{};
   const int D = c.cfg.head_dim;
   memcpy(&f.tmK, c.maps + 16 * MAP_KPAGE, sizeof(CUtensorMap));

@@ -10,6 +10,7 @@
 // result does not depend on timing.
 #pragma once
 
+#include <cooperative_groups.h>
 #include <cudaTypedefs.h>
 
 #include "paged_common.cuh"
@@ -91,6 +92,81 @@ __device__ __forceinline__ void span_of(const Attend& a, const Request& r, int b
   set_span(x, lo, hi, block);
 }
 
+// The end of a block's work on a unit whose keys its warps have shared out: the
+// warps' states (ml: [warps][2][ROWS] maxima and sums; num: numerators, PITCH
+// floats a row, `stride` floats a warp) become the result, a partial result in
+// the scratch, or, in a cluster that shares the unit, the cluster's result.
+struct Settle {
+  int b, h, i0, cells, key0, key1;     // request, KV head, first token, (token, head) rows, keys
+  Request r;
+  int cluster, part;                   // blocks of the cluster (0: none), this block's place
+  bool whole;                          // the unit is this block's alone
+  float* slot;                         // of a partial result
+};
+template <typename T, int D, int ROWS, int PITCH, int WARPS>
+__device__ void settle(const Attend& a, const Settle& s, const float* ml, float* num, int stride, float* unit, int* bad) {
+  namespace cg = cooperative_groups;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t Hq = (int64_t)a.H * a.G;
+  auto final = [&](int row, int c, float m, float l, float v) {
+    const bool none = l == 0.f;
+    const int64_t t = s.r.row0 + s.i0 + row / a.G, hq = s.h * a.G + row % a.G;
+    reinterpret_cast<T*>(a.O + t * a.o_row_b + hq * a.o_head_b)[c] = from_f32<T>(none ? 0.f : v / l);
+    if (a.lse && c == 0) a.lse[t * Hq + hq] = none ? -INFINITY : (m + log2f(l)) / kLog2e;
+  };
+  auto put = [&](int row, int c, float m, float l, float v) {
+    if (s.cluster) {                   // warp 0's numerators are replaced, each by the thread that read it
+      num[row * PITCH + c] = v;
+      if (c == 0) { unit[row] = m; unit[ROWS + row] = l; }
+    } else if (s.whole) {
+      final(row, c, m, l, v);
+    } else {
+      s.slot[2 * ROWS + row * D + c] = v;
+      if (c == 0) { s.slot[row] = m; s.slot[ROWS + row] = l; }
+    }
+  };
+  if (tid < ROWS) bad[tid] = 0;
+  __syncthreads();
+  for (int row = tid / D; row < s.cells; row += WARPS * 32 / D) {
+    const int c = tid % D;
+    float m = -INFINITY, l = 0.f, v = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) m = fmaxf(m, ml[(w * 2) * ROWS + row]);
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      const float mw = ml[(w * 2) * ROWS + row], k = mw == -INFINITY ? 0.f : exp2f(mw - m);
+      l = fmaf(k, ml[(w * 2 + 1) * ROWS + row], l);
+      v = fmaf(k, num[w * stride + row * PITCH + c], v);
+    }
+    // a key that the row does not see can reach its numerator as 0 * (infinity or NaN), and only so
+    if (!isfinite(v) || !isfinite(l)) bad[row] = 1;
+    put(row, c, m, l, v);
+  }
+  __syncthreads();
+  for (int row = warp; row < s.cells; row += WARPS)
+    if (bad[row]) {
+      RowState<T, D> x;
+      attend_row<T, D>(a, s.b, s.r, s.i0 + row / a.G, s.h * a.G + row % a.G, s.key0, s.key1, x);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) put(row, lane * (D / 32) + i, x.m, x.l, x.acc[i]);
+    }
+  if (!s.cluster) return;
+  cg::cluster_group cl = cg::this_cluster();
+  cl.sync();
+  for (int cell = s.part * (WARPS * 32) + tid; cell < s.cells * D; cell += s.cluster * WARPS * 32) {
+    const int row = cell / D, c = cell % D;
+    float m = -INFINITY, l = 0.f, v = 0.f;
+    for (int p = 0; p < s.cluster; ++p) m = fmaxf(m, cl.map_shared_rank(unit, p)[row]);
+    for (int p = 0; p < s.cluster; ++p) {
+      const float mp = cl.map_shared_rank(unit, p)[row], k = mp == -INFINITY ? 0.f : exp2f(mp - m);
+      l = fmaf(k, cl.map_shared_rank(unit, p)[ROWS + row], l);
+      if (k != 0.f) v = fmaf(k, cl.map_shared_rank(num, p)[row * PITCH + c], v);
+    }
+    final(row, c, m, l, v);
+  }
+  cl.sync();                           // no block leaves while its state is read
+}
+
 // Makes the list: tiles of `tile` rows (tokens), blocks of `block` keys.
 cudaError_t launch_work(const Attend& a, const Work& w, int tile, int block, cudaStream_t st);
 // Joins the partial results of cut units: `rows` (token, head) rows a unit, of `tile` tokens.
@@ -102,11 +178,16 @@ constexpr int kFewBlock = 64;                      // keys a block of the share-
 inline int few_rows(int cells) { return cells <= 8 ? 8 : cells <= 16 ? 16 : 32; }
 cudaError_t attend_few(const Attend& a, const mp_paged_cache& c, Work w, int cells, int cluster, cudaStream_t st);
 
+// fp32 (paged_f32.cu): `rows` of 4, 8 or 16 (token, head) rows a tile of `tile` tokens.
+inline int f32_rows(int cells) { return cells <= 4 ? 4 : cells <= 8 ? 8 : 16; }
+cudaError_t attend_f32(const Attend& a, const mp_paged_cache& c, const Work& w, int rows, int tile, int cluster,
+                       cudaStream_t st);
+
 // Many rows (paged_tiles.cu).
 constexpr int kTilesBlock = 128;                   // keys a block of the share-out
 constexpr int kTilesRows = 256;                    // (token, head) rows a unit
 inline int tiles_tokens(int G) { return kTilesRows / G; }
-cudaError_t attend_tiles(const Attend& a, const mp_paged_cache& c, const Work& w, int entries, cudaStream_t st);
+cudaError_t attend_tiles(const Attend& a, const mp_paged_cache& c, const Work& w, cudaStream_t st);
 
 // cuTensorMapEncodeTiled, or null (paged.cu).
 PFN_cuTensorMapEncodeTiled_v12000 map_encoder();
