@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(kF32Warps * 32) f32_kernel(const F32 f) {
   const int part = f.cluster ? (int)(blockIdx.x % f.cluster) : (int)blockIdx.x;
   if (!f.cluster) {
     E0 = f.w.count[0];
-    W = E0 > 0 ? f.w.before[E0] * a.H : 0;
+    W = *reinterpret_cast<const int64_t*>(f.w.count + 2) * a.H;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (W == 0) return;
     N = parts_used(f.w, W);

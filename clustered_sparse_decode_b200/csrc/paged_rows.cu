@@ -169,12 +169,13 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) few_kernel(const __grid_con
         if (part == 0) {
           f.w.before[a.batch] = done;
           f.w.count[0] = a.batch;
+          *reinterpret_cast<int64_t*>(f.w.count + 2) = done;
         }
       }
       __syncthreads();
     }
     E = own ? a.batch : f.w.count[0];
-    W = E > 0 ? before[E] * a.H : 0;
+    W = (own ? before[E] : *reinterpret_cast<const int64_t*>(f.w.count + 2)) * a.H;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (W == 0) return;
     N = parts_used(f.w, W);

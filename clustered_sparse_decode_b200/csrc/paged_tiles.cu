@@ -39,6 +39,8 @@ constexpr int kKeys = kTilesBlock;                 // keys a block (MMA N, then 
 constexpr int kTilesThreads = 384;                 // 2 x 4 softmax warps, MMA, load, two idle
 constexpr int kSoftRegs = 208, kRestRegs = 88;     // 256 * 208 + 128 * 88 <= 384 * 168
 
+constexpr int kItems = 4;                          // items on their way from the loading warp to the others
+
 struct Tiles {
   CUtensorMap tmQ, tmK, tmV;
   Attend a;
@@ -56,8 +58,9 @@ struct TilesCfg {
   static constexpr int OFF_Q = 0;                                     // [2 halves][KT][128 rows][128 B]
   static constexpr int OFF_KV = 2 * STAGE;                            // [NS][KT][128 rows][128 B]
   static constexpr int OFF_BAR = OFF_KV + NS * STAGE;
-  static constexpr int BARS = 2 * NS + 11;
-  static constexpr int USED = OFF_BAR + BARS * 8 + 16;
+  static constexpr int BARS = 2 * NS + 11 + 2 * kItems;
+  static constexpr int OFF_ITEM = (OFF_BAR + BARS * 8 + 4 + 15) / 16 * 16;   // [kItems][16] words
+  static constexpr int USED = OFF_ITEM + kItems * 64;
   static constexpr int SMEM = USED + 1024;
   static_assert(SMEM <= 232448, "shared memory of a block");
 };
@@ -316,6 +319,18 @@ __device__ __forceinline__ float2 exp2_pair(float2 x) {
                                    __int_as_float((__float_as_int(r.y) << 23) + 0x3f800000));
   return mul2(p, scale);
 }
+// tanh(u) / u by a polynomial of u^2 whose relative error on |u| <= 3/4, 2^-25,
+// is the least of its degree (Remez exchange); times u.
+__device__ __forceinline__ float2 tanh_pair(float2 u) {
+  auto c = [](float v) { return make_float2(v, v); };
+  const float2 x = mul2(u, u);
+  float2 p = fma2(c(-0.004716257099062204f), x, c(0.01958290860056877f));
+  p = fma2(p, x, c(-0.05334442853927612f));
+  p = fma2(p, x, c(0.1332540661096573f));
+  p = fma2(p, x, c(-0.33332958817481995f));
+  p = fma2(p, x, c(1.0f));
+  return mul2(p, u);
+}
 template <int N>
 __device__ __forceinline__ float top_of(const float* v) {
   float t[4] = {v[0], v[1], v[2], v[3]};
@@ -350,7 +365,8 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
   const uint32_t sb = sc::smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t kv_full = sb + C::OFF_BAR, kv_empty = kv_full + 8 * NS, q_full = kv_empty + 8 * NS, q_empty = q_full + 8,
-                 s_full = q_empty + 8, p_full = s_full + 16, o_full = p_full + 32, drain = o_full + 16;
+                 s_full = q_empty + 8, p_full = s_full + 16, o_full = p_full + 32, drain = o_full + 16,
+                 item_full = drain + 8, item_empty = item_full + 8 * kItems;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + C::BARS * 8);
 
   if (threadIdx.x == 0) {
@@ -361,6 +377,10 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
     sc::mbar_init(q_full, 1);
     sc::mbar_init(q_empty, 1);
     sc::mbar_init(drain, 1);
+    for (int k = 0; k < kItems; ++k) {
+      sc::mbar_init(item_full + 8 * k, 1);
+      sc::mbar_init(item_empty + 8 * k, 9);              // the softmax warps' and the issuing warp's
+    }
     for (int g = 0; g < 2; ++g) {
       sc::mbar_init(s_full + 8 * g, 1);
       sc::mbar_init(p_full + 16 * g, 4);                 // the first 64 keys' weights, the last's
@@ -382,16 +402,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // this block's share
-  const int E = f.w.count[0];
-  const int64_t W = E > 0 ? f.w.before[E] * a.H : 0;
-  const int N = W > 0 ? parts_used(f.w, W) : 0, part = blockIdx.x;
-  Walk walk{0, 0, 0, 0};
-  if (part < N) {
-    walk.x = walk.start = share(W, N, part);
-    walk.x1 = share(W, N, part + 1);
-    if (walk.x < walk.x1) walk.e = entry_of_warp(f.w.before, E, a.H, walk.x);
-  }
+  const int part = blockIdx.x;
   Item it;
   bool ok = true;
   auto wait_one = [&](uint32_t bar, uint32_t parity) {   // this thread alone; two seconds at most
@@ -412,6 +423,23 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
     return ok = __all_sync(kFull, ok);
   };
 
+  // the n-th item, as the loading warp has written it; false behind the last
+  auto take = [&](uint32_t n) {
+    const uint32_t k = n % kItems;
+    if (!wait(item_full + 8 * k, (n / kItems) & 1u)) return false;
+    const int4* p = reinterpret_cast<const int4*>(smem + C::OFF_ITEM + k * 64);
+    const int4 x = p[0], y = p[1], z = p[2];
+    const int flags = reinterpret_cast<const int*>(p)[12];
+    it.b = x.x; it.h = x.y; it.i0 = x.z; it.key0 = x.w;
+    it.r.row0 = y.x; it.r.n = y.y; it.r.len = y.z; it.nb = y.w;
+    it.from[0] = z.x; it.to[0] = z.y; it.from[1] = z.z; it.to[1] = z.w;
+    it.whole = flags & 1;
+    it.head = flags & 2;
+    __syncwarp();
+    if (lane == 0) sc::mbar_arrive(item_empty + 8 * k);
+    return (flags & 4) == 0;
+  };
+
   if (warp < 8) {
     // ================= softmax: a thread a row =================
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftRegs));
@@ -419,9 +447,11 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t tS = tmem + 128 * g + lanes, tO = tmem + 256 + 128 * g + lanes;
     const float c = a.scale * kLog2e;
-    const float cap2 = a.cap * kLog2e, cap_in = GEN && a.cap > 0.f ? 2.f * c / a.cap : 0.f;   // cap tanh(z / cap) = cap - 2 cap / (1 + e^(2 z / cap))
+    const float cap2 = a.cap * kLog2e, cap_in = GEN && a.cap > 0.f ? 2.f * c / a.cap : 0.f,
+                to_u = GEN && a.cap > 0.f ? a.scale / a.cap : 0.f;
+    const bool straight = !a.full && !a.prefix;          // no row sees a key behind its own   // cap tanh(z / cap) = cap - 2 cap / (1 + e^(2 z / cap))
     uint32_t n_s = 0, n_o = 0, n_kv = 0;                 // phases of s_full and o_full, tiles that have passed the ring
-    while (ok && next_item(f, walk, it)) {
+    for (uint32_t n_item = 0; take(n_item); ++n_item) {
       const int i = it.i0 + g * (f.tile / 2) + row / a.G, hq = it.h * a.G + row % a.G;
       const bool valid = i < it.r.n;
       Interval v{0, INT32_MAX, 0};
@@ -515,16 +545,40 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
             tmem_ld(tS + 32 * k, z);
             tmem_ld_wait(z);
             if (a.cap > 0.f) {
+              // cap tanh(u), u = z / cap: by its exponential (two results of a unit that the weights need too) only
+              // where some |u| of the warp's 32 columns is above 3/4
+              float far = 0.f;
 #pragma unroll
-              for (int q = 0; q < 32; ++q) z[q] = fmaf(-2.f * cap2, rcp(1.f + sc::ex2(z[q] * cap_in)), cap2);
+              for (int q = 0; q < 32; q += 2) far = max3(far, fabsf(z[q]), fabsf(z[q + 1]));
+              if (__any_sync(kFull, far * fabsf(to_u) > 0.75f)) {
+#pragma unroll
+                for (int q = 0; q < 32; ++q) z[q] = fmaf(-2.f * cap2, rcp(1.f + sc::ex2(z[q] * cap_in)), cap2);
+              } else {
+#pragma unroll
+                for (int q = 0; q < 32; q += 2) {
+                  const float2 u = mul2(make_float2(z[q], z[q + 1]), make_float2(to_u, to_u)), y = tanh_pair(u);
+                  z[q] = y.x * cap2;
+                  z[q + 1] = y.y * cap2;
+                }
+              }
             } else {
 #pragma unroll
               for (int q = 0; q < 32; ++q) z[q] *= c;
             }
             if (a.slopes) {
               const float d = ahead - (float)(32 * k);
+              if (__all_sync(kFull, straight || d >= 31.f)) {    // no key behind a row, or none that it sees
+                const float2 at = make_float2(-slope * d, -slope * d), by = make_float2(slope, slope);
 #pragma unroll
-              for (int q = 0; q < 32; ++q) z[q] = fmaf(-slope, fabsf(d - (float)q), z[q]);
+                for (int q = 0; q < 32; q += 2) {
+                  const float2 y = add2(make_float2(z[q], z[q + 1]), fma2(make_float2((float)q, (float)(q + 1)), by, at));
+                  z[q] = y.x;
+                  z[q + 1] = y.y;
+                }
+              } else {
+#pragma unroll
+                for (int q = 0; q < 32; ++q) z[q] = fmaf(-slope, fabsf(d - (float)q), z[q]);
+              }
             }
             if (cut) {
 #pragma unroll
@@ -627,7 +681,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
       const uint32_t acc = __shfl_sync(kFull, tmem, 0);
       uint32_t n_q = 0, n_p0 = 0, n_p1 = 0;
       uint32_t ks = 0, kp = 0;                           // stage and phase of the next K; its V is the next tile
-      while (ok && next_item(f, walk, it)) {
+      for (uint32_t n_item = 0; take(n_item); ++n_item) {
         if (it.to[0] == it.from[0] && it.to[1] == it.from[1]) continue;
         const int from0 = __shfl_sync(kFull, it.from[0], 0), to0 = __shfl_sync(kFull, it.to[0], 0),
                   from1 = __shfl_sync(kFull, it.from[1], 0), to1 = __shfl_sync(kFull, it.to[1], 0),
@@ -688,9 +742,35 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
       }
     } else if (warp == 9) {
       // ================= loads =================
+      // It runs ahead of the others and finds the items for them: the chain of loads that this takes would
+      // otherwise lie between two items of each.
       uint32_t n_kv = 0, n_q = 0, issued = 0;
       const int pg = 1 << a.page_shift, boxes = kKeys / f.box;
-      while (ok && next_item(f, walk, it)) {
+      const int E = f.w.count[0];
+      const int64_t W = *reinterpret_cast<const int64_t*>(f.w.count + 2) * a.H;
+      const int N = W > 0 ? parts_used(f.w, W) : 0;
+      Walk walk{0, 0, 0, 0};
+      if (part < N) {
+        walk.x = walk.start = share(W, N, part);
+        walk.x1 = share(W, N, part + 1);
+        if (walk.x < walk.x1) walk.e = entry_of_warp(f.w.before, E, a.H, walk.x);
+      }
+      for (uint32_t n_item = 0;; ++n_item) {
+        const uint32_t slot = n_item % kItems;
+        const bool more = next_item(f, walk, it);
+        if (n_item >= kItems && !wait(item_empty + 8 * slot, (n_item / kItems - 1) & 1u)) break;
+        if (lane == 0) {
+          int4* p = reinterpret_cast<int4*>(smem + C::OFF_ITEM + slot * 64);
+          if (more) {
+            p[0] = make_int4(it.b, it.h, it.i0, it.key0);
+            p[1] = make_int4(it.r.row0, it.r.n, it.r.len, it.nb);
+            p[2] = make_int4(it.from[0], it.to[0], it.from[1], it.to[1]);
+          }
+          p[3].x = more ? (it.whole ? 1 : 0) | (it.head ? 2 : 0) : 4;
+          sc::mbar_arrive(item_full + 8 * slot);
+        }
+        __syncwarp();
+        if (!more) break;
         const bool used[2] = {it.to[0] > it.from[0], it.to[1] > it.from[1]};
         if (!used[0] && !used[1]) continue;
         if (n_q > 0 && !wait(q_empty, (n_q - 1) & 1u)) break;
@@ -722,6 +802,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
             }
           }
         }
+        if (!ok) break;
         n_kv += 2 * it.nb;
       }
       // copies under way land before the block ends (only after a wait that gave up are there any left)

@@ -23,7 +23,7 @@ struct Entry {
 };
 
 struct Work {
-  int32_t* count;                    // [1] entries
+  int32_t* count;                    // entries; 8 bytes on, as 64 bits: blocks of all, for one head
   int64_t* before;                   // [entries + 1] blocks of the entries before, for one head
   Entry* entry;                      // [entries]
   float* part;                       // [2 parts][rows (2 + D)]: maxima, sums, numerators
