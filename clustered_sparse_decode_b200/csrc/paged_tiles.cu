@@ -54,11 +54,12 @@ struct TilesCfg {
   static constexpr int KT = D / 64;                                   // 64-column panels
   static constexpr int PANEL = kKeys * 128;                           // bytes of a panel of 128 rows
   static constexpr int STAGE = KT * PANEL;
-  static constexpr int NS = 160 * 1024 / STAGE;
-  static constexpr int OFF_Q = 0;                                     // [2 halves][KT][128 rows][128 B]
-  static constexpr int OFF_KV = 2 * STAGE;                            // [NS][KT][128 rows][128 B]
+  static constexpr int QB = D == 64 ? 2 : 1;                          // tiles of Q: the next item's where there is room
+  static constexpr int NS = (224 * 1024 - 2 * QB * STAGE) / STAGE;
+  static constexpr int OFF_Q = 0;                                     // [QB][2 halves][KT][128 rows][128 B]
+  static constexpr int OFF_KV = 2 * QB * STAGE;                       // [NS][KT][128 rows][128 B]
   static constexpr int OFF_BAR = OFF_KV + NS * STAGE;
-  static constexpr int BARS = 2 * NS + 11 + 2 * kItems;
+  static constexpr int BARS = 2 * NS + 9 + 2 * QB + 2 * kItems;
   static constexpr int OFF_ITEM = (OFF_BAR + BARS * 8 + 4 + 15) / 16 * 16;   // [kItems][16] words
   static constexpr int USED = OFF_ITEM + kItems * 64;
   static constexpr int SMEM = USED + 1024;
@@ -319,18 +320,10 @@ __device__ __forceinline__ float2 exp2_pair(float2 x) {
                                    __int_as_float((__float_as_int(r.y) << 23) + 0x3f800000));
   return mul2(p, scale);
 }
-// tanh(u) / u by a polynomial of u^2 whose relative error on |u| <= 3/4, 2^-25,
-// is the least of its degree (Remez exchange); times u.
-__device__ __forceinline__ float2 tanh_pair(float2 u) {
-  auto c = [](float v) { return make_float2(v, v); };
-  const float2 x = mul2(u, u);
-  float2 p = fma2(c(-0.004716257099062204f), x, c(0.01958290860056877f));
-  p = fma2(p, x, c(-0.05334442853927612f));
-  p = fma2(p, x, c(0.1332540661096573f));
-  p = fma2(p, x, c(-0.33332958817481995f));
-  p = fma2(p, x, c(1.0f));
-  return mul2(p, u);
-}
+// tanh(u) / u = sum of kTanh[i] u^(2 i) on |u| <= 3/4: the polynomial of its
+// degree with the least relative error there, 2^-25 (Remez exchange).
+__device__ constexpr float kTanh[6] = {1.0f, -0.33332958817481995f, 0.1332540661096573f, -0.05334442853927612f,
+                                       0.01958290860056877f, -0.004716257099062204f};
 template <int N>
 __device__ __forceinline__ float top_of(const float* v) {
   float t[4] = {v[0], v[1], v[2], v[3]};
@@ -364,8 +357,8 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
   unsigned char* smem = smem_raw + ((1024u - (sc::smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sb = sc::smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t kv_full = sb + C::OFF_BAR, kv_empty = kv_full + 8 * NS, q_full = kv_empty + 8 * NS, q_empty = q_full + 8,
-                 s_full = q_empty + 8, p_full = s_full + 16, o_full = p_full + 32, drain = o_full + 16,
+  const uint32_t kv_full = sb + C::OFF_BAR, kv_empty = kv_full + 8 * NS, q_full = kv_empty + 8 * NS, q_empty = q_full + 8 * C::QB,
+                 s_full = q_empty + 8 * C::QB, p_full = s_full + 16, o_full = p_full + 32, drain = o_full + 16,
                  item_full = drain + 8, item_empty = item_full + 8 * kItems;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + C::BARS * 8);
 
@@ -374,8 +367,10 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
       sc::mbar_init(kv_full + 8 * s, 1);
       sc::mbar_init(kv_empty + 8 * s, 1);
     }
-    sc::mbar_init(q_full, 1);
-    sc::mbar_init(q_empty, 1);
+    for (int k = 0; k < C::QB; ++k) {
+      sc::mbar_init(q_full + 8 * k, 1);
+      sc::mbar_init(q_empty + 8 * k, 1);
+    }
     sc::mbar_init(drain, 1);
     for (int k = 0; k < kItems; ++k) {
       sc::mbar_init(item_full + 8 * k, 1);
@@ -449,6 +444,12 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
     const float c = a.scale * kLog2e;
     const float cap2 = a.cap * kLog2e, cap_in = GEN && a.cap > 0.f ? 2.f * c / a.cap : 0.f,
                 to_u = GEN && a.cap > 0.f ? a.scale / a.cap : 0.f;
+    float capped[6];                                     // cap tanh(s scale / cap) in base 2 as s times a polynomial of s^2
+    {
+      float f = cap2 * to_u;
+#pragma unroll
+      for (int q = 0; q < 6; ++q, f *= to_u * to_u) capped[q] = kTanh[q] * f;
+    }
     const bool straight = !a.full && !a.prefix;          // no row sees a key behind its own   // cap tanh(z / cap) = cap - 2 cap / (1 + e^(2 z / cap))
     uint32_t n_s = 0, n_o = 0, n_kv = 0;                 // phases of s_full and o_full, tiles that have passed the ring
     for (uint32_t n_item = 0; take(n_item); ++n_item) {
@@ -463,6 +464,11 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
         tc_after();
         const int kb = it.key0 + j * kKeys, lo = v.lo - kb, hi = v.hi - kb;
         const bool cut = __any_sync(kFull, v.lo > kb || v.hi < kb + kKeys);
+        // which of the 32 columns from 32 k on this row sees
+        auto seen = [&](int k) {
+          const int from = min(max(lo - 32 * k, 0), 32), to = min(max(hi - 32 * k, 0), 32);
+          return (to == 32 ? ~0u : (1u << to) - 1u) & (from == 32 ? 0u : ~0u << from);
+        };
         // values behind the last token become zeros before a product reads them (the second half's follows the first's)
         auto clear_tail = [&]() {
           if (kb + kKeys <= it.r.len || (g == 1 && j >= it.from[0] && j < it.to[0])) return true;
@@ -522,8 +528,12 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
           for (int k = 0; k < 4; ++k) tmem_ld_wait(s + 32 * k);
           if (cut) {
 #pragma unroll
-            for (int k = 0; k < 128; ++k)
-              if (k < lo || k >= hi) s[k] = -INFINITY;
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t keys = seen(k);
+#pragma unroll
+              for (int q = 0; q < 32; ++q)
+                if (!(keys & 1u << q)) s[32 * k + q] = -INFINITY;
+            }
           }
           raise(top_of<128>(s) * c);
           const float base = m == -INFINITY ? 0.f : -m;
@@ -535,10 +545,10 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
             if (k & 1) hand_over(k >> 1);
           }
         } else {
-          // 32 columns at a time and not unrolled further: the long form would not stay in the instruction cache
-          // (20 us a block instead of 4); the exponents go back to where S was
-          const float ahead = (float)(v.pos - kb);
+          // 32 columns at a time: everything unrolled does not stay in the instruction cache and takes half as long
+          // again.  The exponents go back to where the scores were.
           float mx = -INFINITY;
+          const float ahead = (float)(v.pos - kb);
 #pragma unroll 1
           for (int k = 0; k < 4; ++k) {
             float z[32];
@@ -556,14 +566,23 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
               } else {
 #pragma unroll
                 for (int q = 0; q < 32; q += 2) {
-                  const float2 u = mul2(make_float2(z[q], z[q + 1]), make_float2(to_u, to_u)), y = tanh_pair(u);
-                  z[q] = y.x * cap2;
-                  z[q + 1] = y.y * cap2;
+                  auto c = [](float w) { return make_float2(w, w); };
+                  const float2 u = make_float2(z[q], z[q + 1]), x = mul2(u, u);
+                  float2 y = fma2(c(capped[5]), x, c(capped[4]));
+#pragma unroll
+                  for (int t = 3; t >= 0; --t) y = fma2(y, x, c(capped[t]));
+                  y = mul2(y, u);
+                  z[q] = y.x;
+                  z[q + 1] = y.y;
                 }
               }
             } else {
 #pragma unroll
-              for (int q = 0; q < 32; ++q) z[q] *= c;
+              for (int q = 0; q < 32; q += 2) {
+                const float2 y = mul2(make_float2(z[q], z[q + 1]), make_float2(c, c));
+                z[q] = y.x;
+                z[q + 1] = y.y;
+              }
             }
             if (a.slopes) {
               const float d = ahead - (float)(32 * k);
@@ -581,9 +600,10 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
               }
             }
             if (cut) {
+              const uint32_t keys = seen(k);
 #pragma unroll
               for (int q = 0; q < 32; ++q)
-                if (32 * k + q < lo || 32 * k + q >= hi) z[q] = -INFINITY;
+                if (!(keys & 1u << q)) z[q] = -INFINITY;
             }
             mx = fmaxf(mx, top_of<32>(z));
             tmem_st(tS + 32 * k, reinterpret_cast<const uint32_t*>(z));
@@ -591,14 +611,19 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
           tmem_st_wait();
           raise(mx);
           const float base = m == -INFINITY ? 0.f : -m;
+          const float2 mul = make_float2(1.f, 1.f), sub = make_float2(base, base);
           if (!clear_tail()) break;
+          float z0[32], z1[32];
+          tmem_ld(tS, z0);
 #pragma unroll 1
-          for (int k = 0; k < 4; ++k) {
-            float z[32];
-            tmem_ld(tS + 32 * k, z);
-            tmem_ld_wait(z);
-            weigh(z, k, make_float2(1.f, 1.f), make_float2(base, base));
-            if (k & 1) hand_over(k >> 1);
+          for (int k = 0; k < 4; k += 2) {
+            tmem_ld_wait(z0);
+            tmem_ld(tS + 32 * k + 32, z1);
+            weigh(z0, k, mul, sub);
+            tmem_ld_wait(z1);
+            if (k == 0) tmem_ld(tS + 64, z0);
+            weigh(z1, k + 1, mul, sub);
+            hand_over(k >> 1);
           }
         }
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
@@ -687,9 +712,10 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
                   from1 = __shfl_sync(kFull, it.from[1], 0), to1 = __shfl_sync(kFull, it.to[1], 0),
                   nb = __shfl_sync(kFull, it.nb, 0);
         uint32_t vs = 0, vp = 0;                         // of the V whose products come next
+        const uint32_t qb = n_q % C::QB;
         auto scores = [&](uint32_t g) {                  // S = Q K^T
           tc_after();
-          const uint32_t q = q_lo + g * (C::STAGE >> 4), k = k_lo + ks * (C::STAGE >> 4);
+          const uint32_t q = q_lo + (2 * qb + g) * (C::STAGE >> 4), k = k_lo + ks * (C::STAGE >> 4);
           mma_ss<false>(one, acc + 128 * g, q, k, hi, id_s);
 #pragma unroll
           for (int i = 1; i < D / 16; ++i)
@@ -711,7 +737,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
           if (last) commit(one, o_full + 8 * g);
           return true;
         };
-        ok = wait_one(q_full, n_q & 1u);
+        ok = wait_one(q_full + 8 * qb, (n_q / C::QB) & 1u);
         for (int j = 0; j <= nb && ok; ++j) {
           // a stage is waited for as late and released as early as its products allow
           if (j > 0 && !(ok = wait_one(kv_full + 8 * vs, vp))) break;
@@ -730,7 +756,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
             kp = vp;
             if (ks == NS) { ks = 0; kp ^= 1u; }
           } else {
-            commit(one, q_empty);
+            commit(one, q_empty + 8 * qb);
           }
         }
         ++n_q;
@@ -755,32 +781,40 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
         walk.x1 = share(W, N, part + 1);
         if (walk.x < walk.x1) walk.e = entry_of_warp(f.w.before, E, a.H, walk.x);
       }
-      for (uint32_t n_item = 0;; ++n_item) {
+      uint32_t n_item = 0;
+      auto publish = [&](Item& x) {                      // finds the next item and hands it on
         const uint32_t slot = n_item % kItems;
-        const bool more = next_item(f, walk, it);
-        if (n_item >= kItems && !wait(item_empty + 8 * slot, (n_item / kItems - 1) & 1u)) break;
+        const bool more = next_item(f, walk, x);
+        if (n_item >= kItems && !wait(item_empty + 8 * slot, (n_item / kItems - 1) & 1u)) return false;
+        ++n_item;
         if (lane == 0) {
           int4* p = reinterpret_cast<int4*>(smem + C::OFF_ITEM + slot * 64);
           if (more) {
-            p[0] = make_int4(it.b, it.h, it.i0, it.key0);
-            p[1] = make_int4(it.r.row0, it.r.n, it.r.len, it.nb);
-            p[2] = make_int4(it.from[0], it.to[0], it.from[1], it.to[1]);
+            p[0] = make_int4(x.b, x.h, x.i0, x.key0);
+            p[1] = make_int4(x.r.row0, x.r.n, x.r.len, x.nb);
+            p[2] = make_int4(x.from[0], x.to[0], x.from[1], x.to[1]);
           }
-          p[3].x = more ? (it.whole ? 1 : 0) | (it.head ? 2 : 0) : 4;
+          p[3].x = more ? (x.whole ? 1 : 0) | (x.head ? 2 : 0) : 4;
           sc::mbar_arrive(item_full + 8 * slot);
         }
         __syncwarp();
-        if (!more) break;
+        return more;
+      };
+      for (bool more = publish(it); more && ok;) {
         const bool used[2] = {it.to[0] > it.from[0], it.to[1] > it.from[1]};
-        if (!used[0] && !used[1]) continue;
-        if (n_q > 0 && !wait(q_empty, (n_q - 1) & 1u)) break;
+        if (!used[0] && !used[1]) {
+          more = publish(it);
+          continue;
+        }
+        const uint32_t qb = n_q % C::QB;
+        if (n_q >= C::QB && !wait(q_empty + 8 * qb, (n_q / C::QB - 1) & 1u)) break;
         ++n_q;
         if (lane == 0) {
-          sc::mbar_arrive_tx(q_full, (used[0] ? C::STAGE : 0) + (used[1] ? C::STAGE : 0));
+          sc::mbar_arrive_tx(q_full + 8 * qb, (used[0] ? C::STAGE : 0) + (used[1] ? C::STAGE : 0));
           for (int g = 0; g < 2; ++g)
             for (int k = 0; k < KT && used[g]; ++k)
-              tma_q(sb + C::OFF_Q + g * C::STAGE + k * C::PANEL, &f.tmQ, 64 * k, it.h * a.G,
-                    it.r.row0 + it.i0 + g * (f.tile / 2), q_full);
+              tma_q(sb + C::OFF_Q + (2 * qb + g) * C::STAGE + k * C::PANEL, &f.tmQ, 64 * k, it.h * a.G,
+                    it.r.row0 + it.i0 + g * (f.tile / 2), q_full + 8 * qb);
         }
         for (int j = 0; j < it.nb && ok; ++j) {
           // a lane a box: its keys' page (page 0 in the place of a bad one, whose result does not count)
@@ -804,6 +838,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
         }
         if (!ok) break;
         n_kv += 2 * it.nb;
+        more = publish(it);
       }
       // copies under way land before the block ends (only after a wait that gave up are there any left)
       if (!ok)
