@@ -60,7 +60,7 @@ class MpPagedConfig(ctypes.Structure):
 
 class MpPagedCache(ctypes.Structure):
     _fields_ = [("cfg", MpPagedConfig), ("K", ctypes.c_void_p), ("V", ctypes.c_void_p), ("err", ctypes.c_void_p),
-                ("device", ctypes.c_int32), ("reserved", ctypes.c_int32), ("maps", ctypes.c_uint64 * 64)]
+                ("device", ctypes.c_int32), ("sms", ctypes.c_int32), ("maps", ctypes.c_uint64 * 64)]
 
 
 class MpPagedPlanArgs(ctypes.Structure):

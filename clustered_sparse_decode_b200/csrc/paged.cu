@@ -300,12 +300,6 @@ static mp_status launched() {
   return cudaGetLastError() == cudaSuccess ? MP_OK : MP_ECUDA;
 }
 
-static int sm_count(int device) {
-  int sms = 148;
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
-  return sms;
-}
-
 }  // namespace paged
 }  // namespace mp
 
@@ -343,7 +337,8 @@ mp_status mp_paged_init(const mp_paged_config* cfg, void* K, void* V, int32_t* d
   c.K = K;
   c.V = V;
   c.err = d_err;
-  if (cudaGetDevice(&c.device) != cudaSuccess) {
+  if (cudaGetDevice(&c.device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&c.sms, cudaDevAttrMultiProcessorCount, c.device) != cudaSuccess) {
     cudaGetLastError();
     return MP_ECUDA;
   }
@@ -381,13 +376,14 @@ mp_status mp_paged_plan(const mp_paged_cache* c, const mp_paged_plan_args* p, vo
   const bool in_place = p->lens == p->lens_out || p->free_count == p->free_count_out;
   a.clustered = blocks <= kPlanCluster || in_place;
   const size_t smem = (size_t)(3 * p->batch + 1) * 4;
+  // (the attribute stays set; without more than 40 KB the call would be the dearest part of a step's)
   if (smem > 40 * 1024 &&
       cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
     cudaGetLastError();
     return MP_ECUDA;
   }
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(std::min(blocks, a.clustered ? kPlanCluster : sm_count(c->device)));
+  cfg.gridDim = dim3(std::min(blocks, a.clustered ? kPlanCluster : c->sms));
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
@@ -433,7 +429,7 @@ mp_status mp_paged_append(const mp_paged_cache* c, const void* K_new, const void
   a.limit = (int64_t)c->cfg.num_pages * c->cfg.page_tokens;
   a.err = c->err;
   const int64_t blocks = (a.total + kCopyThreads - 1) / kCopyThreads;
-  const int grid = (int)std::min<int64_t>(blocks, (int64_t)sm_count(c->device) * 8);
+  const int grid = (int)std::min<int64_t>(blocks, (int64_t)c->sms * 8);
   append_kernel<<<grid, kCopyThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
   return launched();
 }
@@ -486,6 +482,8 @@ static mp_status check_attend(const mp_paged_cache* c, const mp_paged_attend_arg
   for (int64_t s : st)
     if (s < 0 || (s * es) % 16 != 0) return MP_EINVAL;
   if ((reinterpret_cast<uintptr_t>(p->Q) | reinterpret_cast<uintptr_t>(p->O)) % 16 != 0) return MP_EINVAL;
+  // rows of O that fall on one another would be written by several blocks
+  if ((p->rows > 1 && p->o_row_stride < g.head_dim) || (p->q_heads > 1 && p->o_head_stride < g.head_dim)) return MP_EINVAL;
   if (!std::isfinite(p->scale) || !std::isfinite(p->softcap) || p->softcap < 0.f || p->window < 0 ||
       (p->flags & ~MP_ATTEND_FULL) != 0)
     return MP_EINVAL;

@@ -49,6 +49,7 @@ static Attend args_of(const mp_paged_cache& c, const mp_paged_attend_args& p) {
   a.first_key = p.first_key;
   a.lse = p.lse;
   a.err = c.err;
+  a.device = c.device;
   return a;
 }
 
@@ -59,7 +60,6 @@ static Attend args_of(const mp_paged_cache& c, const mp_paged_attend_args& p) {
 // shares over all SMs (two or three launches, the same time whatever the
 // lengths).
 constexpr int kFewCells = 32;          // rows that the few-rows kernel takes
-constexpr int kSMs = 148;
 constexpr int kClusterBlocks = 16;     // blocks of keys of a clustered block at most
 
 struct Way {
@@ -76,7 +76,7 @@ static Way way_of(const mp_paged_cache& c, const mp_paged_attend_args& p) {
     w.kind = Way::TILES;
     w.rows = kTilesRows;
     w.tile = tiles_tokens(G);
-    w.parts = kSMs;                    // one block an SM
+    w.parts = c.sms;                   // one block an SM
   } else {
     const bool f32 = c.cfg.dtype == MP_F32;
     w.kind = f32 ? Way::F32 : Way::FEW;
@@ -87,12 +87,12 @@ static Way way_of(const mp_paged_cache& c, const mp_paged_attend_args& p) {
     const int64_t units = (int64_t)p.batch * c.cfg.kv_heads * ((max_new + w.tile - 1) / w.tile);
     const int64_t blocks = ((int64_t)p.table_pages * c.cfg.page_tokens + kFewBlock - 1) / kFewBlock;
     int k = 1;
-    while (k < 8 && units * k < blocks_sm * kSMs) k *= 2;
+    while (k < 8 && units * k < blocks_sm * c.sms) k *= 2;
     if (blocks <= (int64_t)kClusterBlocks * k && units * k <= (1 << 30)) {
       w.cluster = k;
       return w;
     }
-    w.parts = blocks_sm * kSMs;
+    w.parts = blocks_sm * c.sms;
   }
   w.entries = p.rows / w.tile + p.batch;
   return w;

@@ -42,6 +42,7 @@ struct Attend {
   const int32_t* first_key;
   float* lse;
   int32_t* err;
+  int32_t device;
 };
 
 // A request's rows and length, clamped to what the tensors hold: a bad offset

@@ -267,8 +267,6 @@ template <int D, int RH>
 static cudaError_t launch_f32_t(const F32& f, int units, cudaStream_t st) {
   using C = F32Cfg<D, RH>;
   auto kern = f32_kernel<D, RH>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(f.cluster ? units * f.cluster : f.w.parts));
   cfg.blockDim = dim3(kF32Warps * 32);
@@ -285,7 +283,8 @@ static cudaError_t launch_f32_t(const F32& f, int units, cudaStream_t st) {
   }
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, f);
+  static std::atomic<uint64_t> allowed{0};
+  return launch_large(kern, cfg, f, f.a.device, allowed);
 }
 
 template <int D>

@@ -467,8 +467,6 @@ template <typename T, int D, int MT, bool DUP>
 static cudaError_t launch_few_t(Few& f, int units, cudaStream_t st) {
   using C = FewCfg<T, D, MT, DUP>;
   auto kern = few_kernel<T, D, MT, DUP>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(f.cluster ? units * f.cluster : f.w.parts));
   cfg.blockDim = dim3(kFewWarps * 32);
@@ -485,7 +483,8 @@ static cudaError_t launch_few_t(Few& f, int units, cudaStream_t st) {
   }
   cfg.attrs = attr;
   cfg.numAttrs = f.cluster || f.a.batch > kOwnList ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kern, (const Few)f);
+  static std::atomic<uint64_t> allowed{0};
+  return launch_large(kern, cfg, f, f.a.device, allowed);
 }
 
 template <typename T, int D>

@@ -861,8 +861,6 @@ template <typename T, int D, bool GEN>
 static cudaError_t launch_tiles_t(const Tiles& f, cudaStream_t st) {
   using C = TilesCfg<D>;
   auto kern = tiles_kernel<T, D, GEN>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)f.w.parts);
   cfg.blockDim = dim3(kTilesThreads);
@@ -873,7 +871,8 @@ static cudaError_t launch_tiles_t(const Tiles& f, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, f);
+  static std::atomic<uint64_t> allowed{0};
+  return launch_large(kern, cfg, f, f.a.device, allowed);
 }
 
 template <typename T, int D>

@@ -13,6 +13,8 @@
 #include <cooperative_groups.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
+
 #include "paged_common.cuh"
 
 namespace mp {
@@ -67,8 +69,6 @@ __device__ __forceinline__ int entry_of_warp(const int64_t* before, int E, int H
   }
   return lo;
 }
-
-constexpr int kMostParts = 2 * 148;
 
 // An entry's blocks from the keys [lo, hi) that its rows see together.  Rows
 // that see nothing cost a block: their zeros are written.
@@ -188,6 +188,28 @@ constexpr int kTilesBlock = 128;                   // keys a block of the share-
 constexpr int kTilesRows = 256;                    // (token, head) rows a unit
 inline int tiles_tokens(int G) { return kTilesRows / G; }
 cudaError_t attend_tiles(const Attend& a, const mp_paged_cache& c, const Work& w, cudaStream_t st);
+
+// Launches a kernel that needs more shared memory than the default.  The
+// permission costs about as much as a launch and stays with the device's
+// context, so it is asked for once a device, and again if a launch is refused
+// (the context may be a new one).
+template <typename Kernel, typename Args>
+inline cudaError_t launch_large(Kernel* kernel, const cudaLaunchConfig_t& cfg, const Args& args, int device,
+                                std::atomic<uint64_t>& done) {
+  const uint64_t bit = device < 64 ? (uint64_t)1 << device : 0;
+  const bool had = (done.load(std::memory_order_relaxed) & bit) != 0;
+  for (int turn = had ? 1 : 0;; ++turn) {
+    if (turn != 1 || !had) {
+      const cudaError_t e =
+          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
+      if (e != cudaSuccess) return e;
+      done.fetch_or(bit, std::memory_order_relaxed);
+    }
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args);
+    if (e != cudaErrorInvalidValue || turn != 1 || !had) return e;
+    cudaGetLastError();
+  }
+}
 
 // cuTensorMapEncodeTiled, or null (paged.cu).
 PFN_cuTensorMapEncodeTiled_v12000 map_encoder();

@@ -68,16 +68,20 @@ class PagedCache:
         self._index = self.device.index
 
     # ------------------------------------------------------------------ helpers
+    # A decode step's calls take a few microseconds each, most of them here: the
+    # checks read each attribute once and compare plain integers.
     def _run(self, stream, name, f, *args):
         """The call on `stream` (default: the current one) with the cache's device current."""
-        if stream is None and torch.cuda.current_device() == self._index:
-            L.check(f(*args, torch._C._cuda_getCurrentRawStream(self._index)), name)
-            return
-        if stream is not None and stream.device != self.device:
-            raise ValueError(f"the stream belongs to {stream.device}, the cache to {self.device}")
-        with torch.cuda.device(self.device):
-            s = stream if stream is not None else torch.cuda.current_stream()
-            L.check(f(*args, s.cuda_stream), name)
+        if stream is None and torch._C._cuda_getDevice() == self._index:
+            st = f(*args, torch._C._cuda_getCurrentRawStream(self._index))
+        else:
+            if stream is not None and stream.device != self.device:
+                raise ValueError(f"the stream belongs to {stream.device}, the cache to {self.device}")
+            with torch.cuda.device(self.device):
+                s = stream if stream is not None else torch.cuda.current_stream()
+                st = f(*args, s.cuda_stream)
+        if st != L.MP_OK:
+            L.check(st, name)
 
     def _empty(self, stream, shape, dtype):
         """Device memory for a call on `stream`."""
@@ -86,21 +90,28 @@ class PagedCache:
         with torch.cuda.stream(stream):
             return torch.empty(shape, dtype=dtype, device=self.device)
 
-    def _ints(self, t, shape, what, dtype=torch.int32):
-        if t.dtype is not dtype or t.shape != shape or t.device != self.device or not t.is_contiguous():
-            raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {self.device}")
+    def _ints(self, t, n, what, dtype=torch.int32):
+        """The address of a contiguous vector of n integers."""
+        if t.dtype is not dtype or t.numel() != n or t.dim() != 1 or t.get_device() != self._index or not t.is_contiguous():
+            raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {(n,)} on {self.device}")
         return t.data_ptr()
 
     def _table(self, t):
-        if t.dtype is not torch.int32 or t.dim() != 2 or t.device != self.device or (t.shape[1] > 1 and t.stride(1) != 1):
-            raise ValueError(f"the table must be an int32 tensor [requests, pages] on {self.device} with contiguous rows")
-        return t.shape[0], t.shape[1], max(t.stride(0), t.shape[1])
+        if t.dtype is not torch.int32 or t.dim() != 2 or t.get_device() != self._index:
+            raise ValueError(f"the table must be an int32 tensor [requests, pages] on {self.device}")
+        B, W = t.shape
+        row, col = t.stride()
+        if W > 1 and col != 1:
+            raise ValueError("the table's rows must be contiguous")
+        return B, W, max(row, W)
 
     def _rows(self, t, shape, what):
-        if t.dtype is not self.torch_dtype or t.shape != shape or t.device != self.device or t.stride(2) != 1:
+        """Address and strides of [rows, heads, head_dim] whose head rows are contiguous."""
+        s = t.stride()
+        if t.dtype is not self.torch_dtype or t.shape != shape or t.get_device() != self._index or s[2] != 1:
             raise ValueError(f"{what} must be a {self.torch_dtype} tensor of shape {tuple(shape)} on {self.device} "
                              "with contiguous head rows")
-        return t.data_ptr()
+        return t.data_ptr(), s
 
     # ------------------------------------------------------------------ calls
     def new_plan(self, batch, rows):
@@ -128,28 +139,26 @@ class PagedCache:
             else:
                 with torch.cuda.stream(stream):
                     out = self.new_plan(B, rows)
-        T = out.slots.shape[0]
-        if free_pages.dim() != 1:
-            raise ValueError("free_pages must have one axis")
+        T, F = out.slots.numel(), free_pages.numel()
         args = L.PLAN_ARGS.pack(
-            B, W, stride, T, free_pages.shape[0], 0, self._ints(lens, (B,), "lens"),
-            self._ints(new_tokens, (B,), "new_tokens"), table.data_ptr(),
-            self._ints(free_pages, free_pages.shape, "free_pages"), self._ints(free_count, (1,), "free_count"),
-            self._ints(out.lens, (B,), "out.lens"), self._ints(out.cu, (B + 1,), "out.cu"),
-            self._ints(out.slots, (T,), "out.slots", torch.int64), self._ints(out.positions, (T,), "out.positions"),
-            self._ints(out.free_count, (1,), "out.free_count"))
+            B, W, stride, T, F, 0, self._ints(lens, B, "lens"), self._ints(new_tokens, B, "new_tokens"), table.data_ptr(),
+            self._ints(free_pages, F, "free_pages"), self._ints(free_count, 1, "free_count"),
+            self._ints(out.lens, B, "out.lens"), self._ints(out.cu, B + 1, "out.cu"),
+            self._ints(out.slots, T, "out.slots", torch.int64), self._ints(out.positions, T, "out.positions"),
+            self._ints(out.free_count, 1, "out.free_count"))
         self._run(stream, "mp_paged_plan", self.lib.mp_paged_plan, self._h, args)
         return out
 
     def append(self, K_new, V_new, slots, stream=None):
         """Write rows K_new, V_new [rows, kv_heads, head_dim] to their slots (mp_paged_append); slot -1 is skipped."""
-        T = slots.shape[0]
+        T = slots.numel()
         shape = (T, self.kv_heads, self.head_dim)
-        k, v = self._rows(K_new, shape, "K_new"), self._rows(V_new, shape, "V_new")
-        if K_new.stride() != V_new.stride():
+        k, ks = self._rows(K_new, shape, "K_new")
+        v, vs = self._rows(V_new, shape, "V_new")
+        if ks != vs:
             raise ValueError("K_new and V_new need equal strides")
-        self._run(stream, "mp_paged_append", self.lib.mp_paged_append, self._h, k, v, K_new.stride(0), K_new.stride(1),
-                  self._ints(slots, (T,), "slots", torch.int64), T)
+        self._run(stream, "mp_paged_append", self.lib.mp_paged_append, self._h, k, v, ks[0], ks[1],
+                  self._ints(slots, T, "slots", torch.int64), T)
 
     def attend(self, Q, table, lens, cu, max_new=None, scale=0.0, softcap=0.0, window=0, full=False, slopes=None,
                prefix=None, first_key=None, out=None, lse=None, scratch=None, stream=None):
@@ -167,33 +176,41 @@ class PagedCache:
         """
         if Q.dim() != 3:
             raise ValueError("Q must be [rows, heads, head_dim]")
-        T, Hq, d = Q.shape
+        T, Hq, _ = Q.shape
         B, W, stride = self._table(table)
-        q = self._rows(Q, (T, Hq, self.head_dim), "Q")
+        q, qs = self._rows(Q, (T, Hq, self.head_dim), "Q")
         if Hq % self.kv_heads:
             raise ValueError(f"{Hq} query heads over {self.kv_heads} KV heads")
         if out is None:
-            out = self._empty(stream, Q.shape, self.torch_dtype)
-            o = out.data_ptr()
+            if stream is None:
+                out = torch.empty_like(Q)
+            else:
+                out = self._empty(stream, Q.shape, self.torch_dtype)
+            o, os = out.data_ptr(), out.stride()
         else:
-            o = self._rows(out, Q.shape, "out")
+            o, os = self._rows(out, Q.shape, "out")
+        if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (T, Hq) or not lse.is_contiguous()
+                                or lse.get_device() != self._index):
+            raise ValueError(f"lse must be a contiguous float32 tensor of shape {(T, Hq)} on {self.device}")
         args = L.ATTEND_ARGS.pack(
             B, Hq, T, 0 if max_new is None else min(max_new, T), W, stride, table.data_ptr(),
-            self._ints(lens, (B,), "lens"), self._ints(cu, (B + 1,), "cu"), q, o, Q.stride(0), Q.stride(1),
-            out.stride(0), out.stride(1), scale, softcap, window, L.MP_ATTEND_FULL if full else 0,
-            self._ints(slopes, (Hq,), "slopes", torch.float32) if slopes is not None else 0,
-            self._ints(prefix, (B,), "prefix") if prefix is not None else 0,
-            self._ints(first_key, (T,), "first_key") if first_key is not None else 0,
-            self._ints(lse, (T, Hq), "lse", torch.float32) if lse is not None else 0)
+            self._ints(lens, B, "lens"), self._ints(cu, B + 1, "cu"), q, o, qs[0], qs[1], os[0], os[1],
+            scale, softcap, window, L.MP_ATTEND_FULL if full else 0,
+            self._ints(slopes, Hq, "slopes", torch.float32) if slopes is not None else 0,
+            self._ints(prefix, B, "prefix") if prefix is not None else 0,
+            self._ints(first_key, T, "first_key") if first_key is not None else 0,
+            lse.data_ptr() if lse is not None else 0)
         need = ctypes.c_size_t()
         L.check(self.lib.mp_paged_attend_scratch(self._h, args, ctypes.byref(need)), "mp_paged_attend_scratch")
         need = need.value
-        if need and scratch is None:
+        if scratch is not None:
+            s, n = self._ints(scratch, scratch.numel(), "scratch", torch.uint8), scratch.numel()
+        elif need:
             scratch = self._empty(stream, (need,), torch.uint8)
-        elif scratch is not None:
-            self._ints(scratch, scratch.shape, "scratch", torch.uint8)
-        self._run(stream, "mp_paged_attend", self.lib.mp_paged_attend, self._h, args,
-                  scratch.data_ptr() if scratch is not None else 0, scratch.numel() if scratch is not None else 0)
+            s, n = scratch.data_ptr(), need
+        else:
+            s = n = 0
+        self._run(stream, "mp_paged_attend", self.lib.mp_paged_attend, self._h, args, s, n)
         return out
 
     def gather(self, table, lens, n, out=None, stream=None):
@@ -204,12 +221,16 @@ class PagedCache:
         """
         B, W, stride = self._table(table)
         shape = (B, self.kv_heads, n, self.head_dim)
-        K, V = out if out is not None else (self._empty(stream, shape, self.torch_dtype) for _ in range(2))
-        for t in (K, V):
-            if t.shape != shape or t.dtype is not self.torch_dtype or t.device != self.device or not t.is_contiguous():
-                raise ValueError(f"out must be contiguous {self.torch_dtype} tensors of shape {shape} on {self.device}")
+        if out is None:
+            K = self._empty(stream, shape, self.torch_dtype)
+            V = torch.empty_like(K) if stream is None else self._empty(stream, shape, self.torch_dtype)
+        else:
+            K, V = out
+            for t in (K, V):
+                if t.shape != shape or t.dtype is not self.torch_dtype or t.device != self.device or not t.is_contiguous():
+                    raise ValueError(f"out must be contiguous {self.torch_dtype} tensors of shape {shape} on {self.device}")
         self._run(stream, "mp_paged_gather", self.lib.mp_paged_gather, self._h, B, table.data_ptr(), W, stride,
-                  self._ints(lens, (B,), "lens"), n, K.data_ptr(), V.data_ptr())
+                  self._ints(lens, B, "lens"), n, K.data_ptr(), V.data_ptr())
         return K, V
 
     def check_device_error(self, stream=None):

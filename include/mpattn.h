@@ -317,7 +317,7 @@ typedef struct {
   void* V;
   int32_t* err;                      /* the cache's error word (device) */
   int32_t device;
-  int32_t reserved;
+  int32_t sms;                       /* its multiprocessors */
   uint64_t maps[64];                 /* tensor maps (private) */
 } mp_paged_cache;
 

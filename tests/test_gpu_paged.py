@@ -286,6 +286,24 @@ def test_long_and_split(B, Hkv, G, n, new):
     check(c, call(c), c.want())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,most", [(700, 1), (1500, 1), (1500, 40), (600, 3)])
+def test_many_requests(B, most, dtype):
+    """More requests than a block lists itself, and than one round of the list takes; some without rows."""
+    r = np.random.default_rng(B + most)
+    lens = [int(x) for x in r.integers(0, 60, B)]
+    new = [int(min(n, x)) for n, x in zip(lens, r.integers(0, most + 1, B))]
+    c = Case(lens, new, H=1, G=1, d=64, P=16, dtype=dtype, seed=B, width=600)
+    check(c, call(c), c.want())
+
+
+def test_shared_pages():
+    """Two requests whose tables begin with the same pages."""
+    c = Case([64, 80], [1, 20], H=2, G=2, d=64, dtype="bf16", seed=12)
+    c.table[1, :3] = c.table[0, :3]
+    check(c, call(c), c.want())
+
+
 def test_bad_tables_lengths_and_offsets_set_the_error_word():
     c = Case([50, 50], [1, 1], H=1, G=1, d=64)
     cache = cache_of(c)
@@ -345,6 +363,9 @@ def test_refusals():
         with pytest.raises(MpError) as e:
             cache.attend(q, t, lens, cu, **bad)
         assert e.value.status == L.MP_EINVAL
+    with pytest.raises(MpError) as e:                         # rows of the output on one another
+        cache.attend(q, t, lens, cu, out=q[:1].expand(2, 4, 64))
+    assert e.value.status == L.MP_EINVAL
     with pytest.raises(MpError) as e:                         # 3 query heads per KV head
         cache.attend(torch.zeros(2, 6, 64, dtype=torch.bfloat16, device="cuda"), t, lens, cu)
     assert e.value.status == L.MP_EUNSUPPORTED
