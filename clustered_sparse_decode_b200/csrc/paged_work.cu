@@ -72,9 +72,11 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const Attend a, cons
           const Request r = request_of(a, x.b);
           const int prefix = prefix_of(a, x.b), i1 = min(r.n, (x.tile + 1) * tile);
           int lo = INT32_MAX, hi = 0;
-          for (int i = x.tile * tile + lane; i < i1; i += 32) {
-            const Interval v = interval_of(a, r, prefix, i);
-            if (v.hi > v.lo) { lo = min(lo, v.lo); hi = max(hi, v.hi); }
+#pragma unroll 8
+          for (int u = 0; u < (tile + 31) / 32; ++u) {
+            const int i = x.tile * tile + 32 * u + lane;
+            const Interval v = interval_of(a, r, prefix, min(i, i1 - 1));
+            if (i < i1 && v.hi > v.lo) { lo = min(lo, v.lo); hi = max(hi, v.hi); }
           }
           set_span(x, __reduce_min_sync(kFull, lo), __reduce_max_sync(kFull, hi), block);
           if (lane == 0) { spans[0][k] = x.k0; spans[1][k] = x.n; }
