@@ -26,7 +26,8 @@ static inline int elem_bytes16(int dtype) { return dtype == MP_F32 ? 4 : 2; }
 // rows are few, and whenever lengths or count are updated in place) a cluster
 // barrier lies between the blocks' reads of the lengths and the writes of the
 // new ones, so that in and out may be the same memory.  The work is a chain of
-// loads and barriers, not bytes.
+// loads and barriers, not bytes: 4.7 us for 16 requests of a token, 8.4 us for 256
+// prompts of 250,000 tokens (3 MB of slots and positions).
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanCluster = 8;
 constexpr int kPlanBatch = 8192;
@@ -135,8 +136,10 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const Plan a) {
 // Appending: rows [T, H, d] to their slots
 // ---------------------------------------------------------------------------
 // A copy by 16-byte vectors: consecutive threads take consecutive vectors of a
-// row, `kCopies` rows' loads in flight before the first store.  Bound by the
-// memory: each byte is read and written once.
+// row, `kCopies` loads of K and V in flight before the first store.  Bound by the
+// memory, each byte read and written once: 16K tokens (8 heads of 128, bf16) to
+// pages of 16, 134 MB, take 26.6 us, 5.0 TB/s; one, two or four copies in flight and
+// more blocks make no difference of a microsecond.
 constexpr int kCopyThreads = 256;
 constexpr int kCopies = 4;
 
@@ -197,7 +200,8 @@ __global__ void __launch_bounds__(kCopyThreads) append_kernel(const Append a) {
 // Gathering: requests' first n tokens as [B, H, n, d]
 // ---------------------------------------------------------------------------
 // A block copies kGatherRows tokens of one (request, head), K and V, by
-// 16-byte vectors, `kCopies` rows of each thread in flight.
+// 16-byte vectors, `kCopies` rows of each thread in flight: 16 requests of 32K
+// tokens, 4.3 GB, in 653 us, 6.57 TB/s, the rate of a plain copy.
 constexpr int kGatherRows = 128;
 
 struct Gather {

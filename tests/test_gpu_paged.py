@@ -201,7 +201,7 @@ MASKS = [
     dict(window=1), dict(window=20), dict(full=True), dict(full=True, window=50), dict(prefix="half"),
     dict(first_key="documents"), dict(first_key="nothing"), dict(softcap=15.0), dict(slopes="usual"),
     dict(slopes="usual", prefix="half", softcap=30.0), dict(window=40, first_key="documents", prefix="half"),
-    dict(scale=0.02), dict(scale=-0.3, softcap=2.0),
+    dict(scale=0.02), dict(scale=-0.3, softcap=2.0), dict(softcap=1e-3), dict(softcap=1e4, slopes="usual"),
 ]
 
 
