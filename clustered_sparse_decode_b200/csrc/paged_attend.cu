@@ -54,11 +54,11 @@ static Attend args_of(const mp_paged_cache& c, const mp_paged_attend_args& p) {
 }
 
 // How a call is done.  16-bit types with few (token, head) rows a KV head:
-// paged_rows.cu; with more: paged_tiles.cu; fp32: paged_f32.cu.  The first and the
-// last run as clusters of one unit (one launch, no scratch) while a block's part
-// of the longest request that the table can hold stays short, otherwise with
-// shares over all SMs (two or three launches, the same time whatever the
-// lengths).
+// paged_rows.cu; with more: paged_tiles.cu; fp32: paged_f32.cu, which has a kernel
+// for up to 16 rows and one for more.  Few rows run as clusters of one unit (one
+// launch, no scratch) while a block's part of the longest request that the table
+// can hold stays short, otherwise with shares over all SMs (two or three launches,
+// the same time whatever the lengths).
 constexpr int kFewCells = 32;          // rows that the few-rows kernel takes
 constexpr int kClusterBlocks = 16;     // blocks of keys of a clustered block at most
 
@@ -71,7 +71,7 @@ static Way way_of(const mp_paged_cache& c, const mp_paged_attend_args& p) {
   Way w{};
   const int G = p.q_heads / c.cfg.kv_heads, max_new = p.max_new ? p.max_new : p.rows;
   const int64_t cells = (int64_t)max_new * G;
-  w.least = 4;
+  w.least = 1;
   if (c.cfg.dtype != MP_F32 && cells > kFewCells) {
     w.kind = Way::TILES;
     w.rows = kTilesRows;
@@ -83,12 +83,13 @@ static Way way_of(const mp_paged_cache& c, const mp_paged_attend_args& p) {
     w.cells = (int)(cells < 32 ? cells : 32);
     w.rows = f32 ? f32_rows(w.cells) : few_rows(w.cells);
     w.tile = f32 ? w.rows / G : max_new;
-    const int blocks_sm = f32 ? 1 : 2;
+    const bool many = f32 && w.rows == kF32ManyRows;
+    const int blocks_sm = f32 && !many ? 1 : 2;
     const int64_t units = (int64_t)p.batch * c.cfg.kv_heads * ((max_new + w.tile - 1) / w.tile);
     const int64_t blocks = ((int64_t)p.table_pages * c.cfg.page_tokens + kFewBlock - 1) / kFewBlock;
     int k = 1;
     while (k < 8 && units * k < blocks_sm * c.sms) k *= 2;
-    if (blocks <= (int64_t)kClusterBlocks * k && units * k <= (1 << 30)) {
+    if (!many && blocks <= (int64_t)kClusterBlocks * k && units * k <= (1 << 30)) {
       w.cluster = k;
       return w;
     }

@@ -183,8 +183,8 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) few_kernel(const __grid_con
     if (W == 0) return;
     N = parts_used(f.w, W);
     if (part >= N) return;
-    x = share(W, N, part);
-    x1 = share(W, N, part + 1);
+    x = edge<false>(before, E, a.H, W, N, part);
+    x1 = edge<false>(before, E, a.H, W, N, part + 1);
     if (x >= x1) return;
     e = entry_of(before, E, a.H, x);
   } else {

@@ -783,8 +783,8 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
       const int N = W > 0 ? parts_used(f.w, W) : 0;
       Walk walk{0, 0, 0, 0};
       if (part < N) {
-        walk.x = walk.start = share(W, N, part);
-        walk.x1 = share(W, N, part + 1);
+        walk.x = walk.start = edge<true>(f.w.before, E, a.H, W, N, part);
+        walk.x1 = edge<true>(f.w.before, E, a.H, W, N, part + 1);
         if (walk.x < walk.x1) walk.e = entry_of_warp(f.w.before, E, a.H, walk.x);
       }
       uint32_t n_item = 0;

@@ -131,13 +131,15 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Attend a, c
   if (W == 0) return;
   const int N = parts_used(w, W);
   if (c >= N) return;
-  const int64_t x = share(W, N, c), before = share(W, N, c - 1);
+  const int64_t x = share(W, N, c);
   const int e = entry_of_warp(w.before, count, a.H, x);
   const int64_t first = w.before[e] * a.H, n = w.before[e + 1] - w.before[e];
   const Entry en = w.entry[e];
   const int h = (int)((x - first) / n);
   const int64_t u0 = first + h * n, u1 = u0 + n;
-  if (x == u0 || before > u0) return;          // a boundary between units, or not this unit's first
+  // an edge between units, of a unit that is not cut, or not the first inside its unit
+  if (x == u0 || n <= kWholeBlocks || share(W, N, c - 1) > u0) return;
+  const int64_t before = edge<true>(w.before, count, a.H, W, N, c - 1);
   const int c1 = part_of(W, N, u1 - 1), np = c1 - c + 2;
   const Request r = request_of(a, en.b);
   const int cells = min(tile, r.n - en.tile * tile) * a.G, lane = threadIdx.x & 31;

@@ -4,8 +4,9 @@
 // blocks that its rows can see.  With H heads, the units (entry, head) laid
 // end to end, blocks inside, are one line of W blocks, of which part c of N
 // gets [c W / N, (c + 1) W / N): equal shares whatever the requests' lengths,
-// most units whole.  A unit cut between parts leaves a partial result in each
-// (two at most a part: the unit its share begins inside of, and the one it
+// most units whole, and those of up to kWholeBlocks blocks always (an edge inside
+// one moves to its nearer end).  A unit cut between parts leaves a partial result
+// in each (two at most a part: the unit its share begins inside of, and the one it
 // ends inside of), and a second kernel joins them in the parts' order, so the
 // result does not depend on timing.
 #pragma once
@@ -39,13 +40,14 @@ __device__ __forceinline__ int parts_used(const Work& w, int64_t W) {
   const int64_t n = (W + w.least - 1) / w.least;
   return (int)(n < w.parts ? (n < 1 ? 1 : n) : w.parts);
 }
-// the part that block x of the line belongs to
+// the last part whose share begins at or before block x
 __device__ __forceinline__ int part_of(int64_t W, int N, int64_t x) {
   int c = (int)(x * N / W);
   while (c + 1 < N && share(W, N, c + 1) <= x) ++c;
   while (c > 0 && share(W, N, c) > x) --c;
   return c;
 }
+constexpr int kWholeBlocks = 4;      // two joined parts of a unit cost more than so many blocks
 // the entry that block x of the line belongs to
 __device__ __forceinline__ int entry_of(const int64_t* before, int E, int H, int64_t x) {
   int lo = 0, hi = E;
@@ -167,6 +169,18 @@ __device__ void settle(const Attend& a, const Settle& s, const float* ml, float*
   cl.sync();                           // no block leaves while its state is read
 }
 
+// where part c begins: by a thread, or by the lanes of a warp together
+template <bool WARP>
+__device__ __forceinline__ int64_t edge(const int64_t* before, int E, int H, int64_t W, int N, int c) {
+  const int64_t x = share(W, N, c);
+  if (x <= 0 || x >= W) return x;
+  const int e = WARP ? entry_of_warp(before, E, H, x) : entry_of(before, E, H, x);
+  const int64_t n = before[e + 1] - before[e];
+  if (n > kWholeBlocks) return x;
+  const int64_t in = (x - before[e] * H) % n;
+  return 2 * in < n ? x - in : x - in + n;
+}
+
 // Makes the list: tiles of `tile` rows (tokens), blocks of `block` keys.
 cudaError_t launch_work(const Attend& a, const Work& w, int tile, int block, cudaStream_t st);
 // Joins the partial results of cut units: `rows` (token, head) rows a unit, of `tile` tokens.
@@ -178,8 +192,9 @@ constexpr int kFewBlock = 64;                      // keys a block of the share-
 inline int few_rows(int cells) { return cells <= 8 ? 8 : cells <= 16 ? 16 : 32; }
 cudaError_t attend_few(const Attend& a, const mp_paged_cache& c, Work w, int cells, int cluster, cudaStream_t st);
 
-// fp32 (paged_f32.cu): `rows` of 4, 8 or 16 (token, head) rows a tile of `tile` tokens.
-inline int f32_rows(int cells) { return cells <= 4 ? 4 : cells <= 8 ? 8 : 16; }
+// fp32 (paged_f32.cu): `rows` of 4, 8, 16 or 64 (token, head) rows a tile of `tile` tokens.
+constexpr int kF32ManyRows = 64;
+inline int f32_rows(int64_t cells) { return cells <= 4 ? 4 : cells <= 8 ? 8 : cells <= 16 ? 16 : kF32ManyRows; }
 cudaError_t attend_f32(const Attend& a, const mp_paged_cache& c, const Work& w, int rows, int tile, int cluster,
                        cudaStream_t st);
 
