@@ -288,7 +288,8 @@ struct ManyCfg {
   static constexpr int STAGE = kManyTile * (KP + D) * 4;
   static constexpr int OFF_Q = 2 * STAGE;                             // [64 rows][D]
   static constexpr int OFF_P = OFF_Q + kManyRows * D * 4;             // [warps][32 keys][8 rows]
-  static constexpr int SMEM = OFF_P + kManyWarps * kManyTile * kManyHeld * 4;
+  static constexpr int OFF_ROW = OFF_P + kManyWarps * kManyTile * kManyHeld * 4;   // [64 rows] first key, end, position, slope
+  static constexpr int SMEM = OFF_ROW + kManyRows * 16;
   static_assert(2 * SMEM <= 225 * 1024, "two blocks an SM");
 };
 
@@ -302,6 +303,7 @@ __global__ void __launch_bounds__(kManyWarps * 32, 2) f32_many_kernel(const F32 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   float* q = reinterpret_cast<float*>(smem + C::OFF_Q) + warp * RW * D;
   float* pw = reinterpret_cast<float*>(smem + C::OFF_P) + warp * kManyTile * RW;
+  int4* rows = reinterpret_cast<int4*>(smem + C::OFF_ROW) + warp * RW;
   const uint32_t base = sc::smem_u32(smem);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -325,24 +327,22 @@ __global__ void __launch_bounds__(kManyWarps * 32, 2) f32_many_kernel(const F32 
     const int i0 = en.tile * f.tile, cells = min(r.n - i0, f.tile) * a.G, prefix = prefix_of(a, en.b);
     const int key0 = en.k0 + (int)(x - u0) * kFewBlock;
     // the warp's rows, and the keys they see together
-    int lo[RW], hi[RW], pos[RW], from = INT32_MAX, to = 0;
-    float slope[RW];
-#pragma unroll
-    for (int k = 0; k < RW; ++k) {
-      const int row = warp * RW + k;
-      lo[k] = hi[k] = pos[k] = 0;
-      slope[k] = 0.f;
-      if (row >= cells) continue;
-      const Interval v = interval_of(a, r, prefix, i0 + row / a.G);
-      lo[k] = v.lo;
-      hi[k] = v.hi;
-      pos[k] = v.pos;
-      if (a.slopes) slope[k] = __ldg(a.slopes + h * a.G + row % a.G);
-      if (v.hi > v.lo) {
-        from = min(from, v.lo);
-        to = max(to, v.hi);
+    int from = INT32_MAX, to = 0;
+    if (lane < RW) {
+      const int row = warp * RW + lane;
+      int4 x4 = make_int4(0, 0, 0, 0);
+      if (row < cells) {
+        const Interval v = interval_of(a, r, prefix, i0 + row / a.G);
+        x4 = make_int4(v.lo, v.hi, v.pos, a.slopes ? __float_as_int(__ldg(a.slopes + h * a.G + row % a.G)) : 0);
+        if (v.hi > v.lo) {
+          from = v.lo;
+          to = v.hi;
+        }
       }
+      rows[lane] = x4;
     }
+    from = __reduce_min_sync(kFull, from);
+    to = __reduce_max_sync(kFull, to);
     for (int c = tid; c < kManyRows * D / 4; c += kManyWarps * 32) {
       const int row = c / (D / 4), d = c % (D / 4);
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -352,27 +352,34 @@ __global__ void __launch_bounds__(kManyWarps * 32, 2) f32_many_kernel(const F32 
       reinterpret_cast<float4*>(smem + C::OFF_Q)[c] = v;
     }
     const int tiles = (int)(end - x) * (kFewBlock / kManyTile);
-    uint32_t empty = 0;                // stages whose pages are bad: nothing of them is used (both halves of a tile)
+    uint32_t empty = 0;                // halves of the stages' tiles whose page is bad: nothing of them is used
+    // a tile lies in one page or in two of 16 tokens; their numbers are asked for a tile ahead of its loads
+    const int32_t* table = a.table + (int64_t)en.b * a.table_stride;
+    int page0 = 0, page1 = 0;
+    auto look_up = [&](int t) {
+      const int j = key0 + t * kManyTile;
+      page0 = t < tiles && j < r.len ? __ldg(table + (j >> a.page_shift)) : 0;
+      page1 = t < tiles && j + 16 < r.len ? __ldg(table + ((j + 16) >> a.page_shift)) : 0;
+    };
     auto fetch = [&](int t) {          // always one group
       if (t < tiles) {
-        const int j0 = key0 + t * kManyTile, s = t & 1;
-        int64_t at[2];                 // a tile lies in one page or in two of 16 tokens
+        const int j0 = key0 + t * kManyTile, s = t & 1, mask = (1 << a.page_shift) - 1;
+        const bool bad0 = (unsigned)page0 >= (unsigned)a.num_pages, bad1 = (unsigned)page1 >= (unsigned)a.num_pages;
+        if (bad0 || bad1) set_error(a.err, E_BAD_OFFSET);
+        empty = (empty & ~(3u << (2 * s))) | (bad0 ? 1u << (2 * s) : 0u) | (bad1 ? 2u << (2 * s) : 0u);
+        const int64_t at0 = page0 * a.page_b + h * a.head_b + (j0 & mask) * a.tok_b,
+                      at1 = page1 * a.page_b + h * a.head_b + ((j0 + 16) & mask) * a.tok_b;
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const int j = j0 + 16 * p, page = j < r.len ? page_of(a, en.b, j) : -1;
-          at[p] = page < 0 ? -1 : page * a.page_b + h * a.head_b + (j & ((1 << a.page_shift) - 1)) * a.tok_b;
-          const uint32_t bit = 1u << (2 * s + p);
-          empty = page < 0 ? empty | bit : empty & ~bit;
-        }
         for (int c = tid; c < kManyTile * D / 4; c += kManyWarps * 32) {
           const int row = c / (D / 4), d = c % (D / 4);
-          const bool in = at[row >> 4] >= 0 && j0 + row < r.len;
-          const int64_t src = in ? at[row >> 4] + (row & 15) * a.tok_b + d * 16 : 0;
+          const bool in = !(row < 16 ? bad0 : bad1) && j0 + row < r.len;
+          const int64_t src = in ? (row < 16 ? at0 : at1) + (row & 15) * a.tok_b + d * 16 : 0;
           sc::cp16(base + s * C::STAGE + (row * C::KP + d * 4) * 4, a.K + src, in);
           sc::cp16(base + s * C::STAGE + (kManyTile * C::KP + row * D + d * 4) * 4, a.V + src, in);
         }
       }
       sc::cp_commit();
+      look_up(t + 1);
     };
     float acc[RW][E], m[RW], l[RW];
 #pragma unroll
@@ -382,6 +389,7 @@ __global__ void __launch_bounds__(kManyWarps * 32, 2) f32_many_kernel(const F32 
 #pragma unroll
       for (int c = 0; c < E; ++c) acc[k][c] = 0.f;
     }
+    look_up(0);
     fetch(0);
     for (int t = 0; t < tiles; ++t) {
       fetch(t + 1);
@@ -407,7 +415,8 @@ __global__ void __launch_bounds__(kManyWarps * 32, 2) f32_many_kernel(const F32 
         bool grow = false;
 #pragma unroll
         for (int k = 0; k < RW; ++k) {
-          z[k] = !held || j < lo[k] || j >= hi[k] ? -INFINITY : score2(a, z[k], slope[k], pos[k] - j);
+          const int4 v = rows[k];
+          z[k] = !held || j < v.x || j >= v.y ? -INFINITY : score2(a, z[k], __int_as_float(v.w), v.z - j);
           grow |= z[k] > m[k] + 8.f;
         }
         if (__any_sync(kFull, grow)) {
