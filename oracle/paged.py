@@ -1,4 +1,4 @@
-"""Paged-cache operators in plain numpy, 64 bits: the checker of the GPU calls.
+"""The oracle of the paged-cache calls: plain numpy, 64 bits.
 
 Shares no code with the CUDA path.  Arrays: K, V [pages, H, P, d]; table
 [B, W]; a request's token at position p lies in page table[b][p // P], row p % P.
