@@ -409,6 +409,8 @@ mp_status mp_paged_append(const mp_paged_cache* c, const void* K_new, const void
   if (!c || rows < 0) return MP_EINVAL;
   if (rows > 0 && (!K_new || !V_new || !slots)) return MP_EINVAL;
   const int es = elem_bytes16(c->cfg.dtype);
+  if (rows <= 1) row_stride = 0;                   // the stride of an axis of length 1 means nothing
+  if (c->cfg.kv_heads == 1) head_stride = 0;
   if (row_stride < 0 || head_stride < 0 || (row_stride * es) % 16 != 0 || (head_stride * es) % 16 != 0 ||
       (reinterpret_cast<uintptr_t>(K_new) | reinterpret_cast<uintptr_t>(V_new)) % 16 != 0)
     return MP_EINVAL;
@@ -482,9 +484,12 @@ static mp_status check_attend(const mp_paged_cache* c, const mp_paged_attend_arg
   if (p->batch > 0 && p->rows > 0 && (!p->lens || !p->cu || !p->Q || !p->O || (p->table_pages > 0 && !p->table)))
     return MP_EINVAL;
   const int es = elem_bytes16(g.dtype);
-  const int64_t st[4] = {p->q_row_stride, p->q_head_stride, p->o_row_stride, p->o_head_stride};
-  for (int64_t s : st)
-    if (s < 0 || (s * es) % 16 != 0) return MP_EINVAL;
+  // (the stride of an axis of length 1 means nothing)
+  const int64_t rows_st[2] = {p->q_row_stride, p->o_row_stride}, heads_st[2] = {p->q_head_stride, p->o_head_stride};
+  for (int i = 0; i < 2; ++i) {
+    if (p->rows > 1 && (rows_st[i] < 0 || (rows_st[i] * es) % 16 != 0)) return MP_EINVAL;
+    if (p->q_heads > 1 && (heads_st[i] < 0 || (heads_st[i] * es) % 16 != 0)) return MP_EINVAL;
+  }
   if ((reinterpret_cast<uintptr_t>(p->Q) | reinterpret_cast<uintptr_t>(p->O)) % 16 != 0) return MP_EINVAL;
   // rows of O that fall on one another would be written by several blocks
   if ((p->rows > 1 && p->o_row_stride < g.head_dim) || (p->q_heads > 1 && p->o_head_stride < g.head_dim)) return MP_EINVAL;

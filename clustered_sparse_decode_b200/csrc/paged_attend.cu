@@ -40,6 +40,9 @@ static Attend args_of(const mp_paged_cache& c, const mp_paged_attend_args& p) {
   a.q_head_b = p.q_head_stride * es;
   a.o_row_b = p.o_row_stride * es;
   a.o_head_b = p.o_head_stride * es;
+  const int64_t row = (int64_t)p.q_heads * g.head_dim * es;    // in the place of strides that mean nothing
+  if (p.rows == 1) a.q_row_b = a.o_row_b = row;
+  if (p.q_heads == 1) a.q_head_b = a.o_head_b = row;
   a.scale = p.scale != 0.f ? p.scale : 1.f / sqrtf((float)g.head_dim);
   a.cap = p.softcap;
   a.window = std::min(p.window, 1 << 30);

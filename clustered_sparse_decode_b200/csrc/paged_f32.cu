@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kF32Warps * 32) f32_kernel(const F32 f) {
     blk0 = f.cluster ? (int)((int64_t)en.n * part / f.cluster) : (int)(x - u0);
     blk1 = f.cluster ? (int)((int64_t)en.n * (part + 1) / f.cluster) : (int)(min(x1, u1) - u0);
     // this lane's rows
-    int lo[RH], hi[RH], pos[RH], top = 0;
+    int lo[RH], hi[RH], pos[RH], low = INT32_MAX, top = 0;
     float slope[RH];
 #pragma unroll
     for (int k = 0; k < RH; ++k) {
@@ -123,8 +123,12 @@ __global__ void __launch_bounds__(kF32Warps * 32) f32_kernel(const F32 f) {
       hi[k] = v.hi;
       pos[k] = v.pos;
       if (a.slopes) slope[k] = __ldg(a.slopes + st.h * a.G + row % a.G);
-      if (v.hi > v.lo) top = max(top, v.hi);
+      if (v.hi > v.lo) {
+        low = min(low, v.lo);
+        top = max(top, v.hi);
+      }
     }
+    low = __reduce_min_sync(kFull, low);
     top = __reduce_max_sync(kFull, top);
     st.key0 = k0 + blk0 * kFewBlock;
     st.key1 = min(k0 + blk1 * kFewBlock, top);
@@ -145,7 +149,8 @@ __global__ void __launch_bounds__(kF32Warps * 32) f32_kernel(const F32 f) {
     uint32_t void_stages = 0;
     auto fetch = [&](int i) {          // always one group, empty behind the last tile
       if (i < tiles) {
-        if ((i & 31) == 0) pages = i + lane < tiles ? page_of(a, en.b, first + (i + lane) * kFewBlock) : -1;
+        if ((i & 31) == 0) pages = i + lane < tiles && first + (i + lane) * kFewBlock + kF32Tile > low    // unseen: maybe no page
+                                      ? page_of(a, en.b, first + (i + lane) * kFewBlock) : -1;
         const int page = __shfl_sync(kFull, pages, i & 31), j = first + i * kFewBlock, s = i % NS;
         void_stages = page < 0 ? void_stages | 1u << s : void_stages & ~(1u << s);
         if (page >= 0) {
@@ -344,6 +349,16 @@ __global__ void __launch_bounds__(kManyWarps * 32, 2) f32_many_kernel(const F32 
     }
     from = __reduce_min_sync(kFull, from);
     to = __reduce_max_sync(kFull, to);
+    int low = INT32_MAX, top = 0;      // keys that any row of the block sees
+    for (int row = lane; row < cells; row += 32) {
+      const Interval v = interval_of(a, r, prefix, i0 + row / a.G);
+      if (v.hi > v.lo) {
+        low = min(low, v.lo);
+        top = max(top, v.hi);
+      }
+    }
+    low = __reduce_min_sync(kFull, low);
+    top = __reduce_max_sync(kFull, top);
     for (int c = tid; c < kManyRows * D / 4; c += kManyWarps * 32) {
       const int row = c / (D / 4), d = c % (D / 4);
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -356,20 +371,23 @@ __global__ void __launch_bounds__(kManyWarps * 32, 2) f32_many_kernel(const F32 
     uint32_t empty = 0;                // halves of the stages' tiles whose page is bad: nothing of them is used
     // a tile lies in one page or in two of 16 tokens; their numbers are asked for a tile ahead of its loads
     const int32_t* table = a.table + (int64_t)en.b * a.table_stride;
-    int page0 = 0, page1 = 0;
+    // (one that no row sees counts as empty: its table entry need not be valid any more)
+    constexpr int kUnseen = INT32_MIN;
+    int page0 = kUnseen, page1 = kUnseen;
     auto look_up = [&](int t) {
       const int j = key0 + t * kManyTile;
-      page0 = t < tiles && j < r.len ? __ldg(table + (j >> a.page_shift)) : 0;
-      page1 = t < tiles && j + 16 < r.len ? __ldg(table + ((j + 16) >> a.page_shift)) : 0;
+      const bool see0 = t < tiles && j < top && j + 16 > low, see1 = t < tiles && j + 16 < top && j + 32 > low;
+      page0 = see0 ? __ldg(table + (j >> a.page_shift)) : kUnseen;
+      page1 = see1 ? __ldg(table + ((j + 16) >> a.page_shift)) : kUnseen;
     };
     auto fetch = [&](int t) {          // always one group
       if (t < tiles) {
         const int j0 = key0 + t * kManyTile, s = t & 1, mask = (1 << a.page_shift) - 1;
         const bool bad0 = (unsigned)page0 >= (unsigned)a.num_pages, bad1 = (unsigned)page1 >= (unsigned)a.num_pages;
-        if (bad0 || bad1) set_error(a.err, E_BAD_OFFSET);
+        if ((bad0 && page0 != kUnseen) || (bad1 && page1 != kUnseen)) set_error(a.err, E_BAD_OFFSET);
         empty = (empty & ~(3u << (2 * s))) | (bad0 ? 1u << (2 * s) : 0u) | (bad1 ? 2u << (2 * s) : 0u);
-        const int64_t at0 = page0 * a.page_b + h * a.head_b + (j0 & mask) * a.tok_b,
-                      at1 = page1 * a.page_b + h * a.head_b + ((j0 + 16) & mask) * a.tok_b;
+        const int64_t at0 = (bad0 ? 0 : page0) * a.page_b + h * a.head_b + (j0 & mask) * a.tok_b,
+                      at1 = (bad1 ? 0 : page1) * a.page_b + h * a.head_b + ((j0 + 16) & mask) * a.tok_b;
 #pragma unroll
         for (int c = tid; c < kManyTile * D / 4; c += kManyWarps * 32) {
           const int row = c / (D / 4), d = c % (D / 4);

@@ -277,8 +277,8 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) few_kernel(const __grid_con
     uint32_t void_stages = 0;          // stages whose tile has no page
     auto fetch = [&](int i) {
       if ((i & 31) == 0) {
-        const int j = first + (i + lane) * kFewBlock;
-        pages = i + lane < tiles ? page_of(a, b, j) : -1;
+        const int j = first + (i + lane) * kFewBlock;    // a tile that no row sees may have no page any more
+        pages = i + lane < tiles && j + kTile > lo_min ? page_of(a, b, j) : -1;
       }
       const int page = __shfl_sync(kFull, pages, i & 31), j = first + i * kFewBlock;
       const uint32_t s = fills % NS;

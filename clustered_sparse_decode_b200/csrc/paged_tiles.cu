@@ -197,6 +197,7 @@ struct Item {
   Request r;
   int key0, nb;                        // first key, blocks
   int from[2], to[2];                  // blocks that each half's rows can see ([0, 0): none)
+  int lo, hi;                          // keys that any of its rows sees (the loading warp's alone)
   bool whole, head;                    // the unit is not cut; the share begins with this item
   int64_t next;
 };
@@ -224,6 +225,8 @@ __device__ __forceinline__ bool next_item(const Tiles& f, Walk& w, Item& it) {
   it.whole = w.x == u0 && end == u1;
   it.head = w.x == w.start;
   const int prefix = prefix_of(a, en.b);
+  it.lo = INT32_MAX;
+  it.hi = 0;
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
     int lo = INT32_MAX, hi = 0;
@@ -237,6 +240,8 @@ __device__ __forceinline__ bool next_item(const Tiles& f, Walk& w, Item& it) {
     }
     lo = __reduce_min_sync(kFull, lo);
     hi = __reduce_max_sync(kFull, hi);
+    it.lo = min(it.lo, lo);
+    it.hi = max(it.hi, hi);
     it.from[g] = hi > lo ? max(0, min(it.nb, (lo - it.key0) >> 7)) : 0;
     it.to[g] = hi > lo ? max(0, min(it.nb, (hi - it.key0 + kKeys - 1) >> 7)) : 0;
     if (it.to[g] <= it.from[g]) it.from[g] = it.to[g] = 0;
@@ -823,10 +828,12 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
                     it.r.row0 + it.i0 + g * (f.tile / 2), q_full + 8 * qb);
         }
         for (int j = 0; j < it.nb && ok; ++j) {
-          // a lane a box: its keys' page (page 0 in the place of a bad one, whose result does not count)
+          // a lane a box: its keys' page (page 0 in the place of a bad one, whose result does not count; a neighbour
+          // that is seen in the place of one that is not, whose table entry need not be valid any more)
           const int key = it.key0 + j * kKeys + lane * f.box;
           const bool mine = lane < boxes && key < it.r.len;
-          const int page = mine ? max(0, page_of(a, it.b, key)) : 0;
+          const int known = min(max(key, it.lo), it.hi - 1);
+          const int page = mine ? max(0, page_of(a, it.b, known)) : 0;
           const uint32_t bytes = __popc(__ballot_sync(kFull, mine)) * (uint32_t)f.box * D * 2;
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {

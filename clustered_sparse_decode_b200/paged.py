@@ -101,9 +101,9 @@ class PagedCache:
             raise ValueError(f"the table must be an int32 tensor [requests, pages] on {self.device}")
         B, W = t.shape
         row, col = t.stride()
-        if W > 1 and col != 1:
-            raise ValueError("the table's rows must be contiguous")
-        return B, W, max(row, W)
+        if (W > 1 and col != 1) or (B > 1 and row < W):
+            raise ValueError("the table's rows must be contiguous and apart from one another")
+        return B, W, row if B > 1 else W
 
     def _rows(self, t, shape, what):
         """Address and strides of [rows, heads, head_dim] whose head rows are contiguous."""
@@ -115,7 +115,7 @@ class PagedCache:
 
     # ------------------------------------------------------------------ calls
     def new_plan(self, batch, rows):
-        """Buffers of plan(out=...) for up to `batch` requests and `rows` rows."""
+        """Buffers of plan(out=...) for `batch` requests and `rows` rows."""
         i32 = dict(dtype=torch.int32, device=self.device)
         return PagedPlan(torch.empty(batch, **i32), torch.empty(batch + 1, **i32),
                          torch.empty(rows, dtype=torch.int64, device=self.device), torch.empty(rows, **i32),

@@ -392,7 +392,9 @@ mp_status mp_paged_append(const mp_paged_cache* cache, const void* K_new, const 
  * position p (above) sees the keys j in [lo, hi), hi = max(p + 1, min(prefix,
  * len)) or len with MP_ATTEND_FULL, lo = max(first_key, p - window + 1);
  * z_j = scale q.k_j, capped, biased; O = sum e^z v / sum e^z over the keys it
- * sees, whatever other keys hold; 0 for a row that sees none.  Rows from
+ * sees, whatever other keys hold; 0 for a row that sees none.  Table entries of
+ * pages before the first key that a request's rows see, and behind its len, are
+ * not followed (a sliding window's pages may be given away).  Rows from
  * cu[batch] on are left as they were.  Accumulation and softmax are fp32.
  * `d_scratch` (256-byte aligned, mp_paged_attend_scratch bytes, contents
  * irrelevant) holds the partial results of one call at a time. */

@@ -297,6 +297,31 @@ def test_many_requests(B, most, dtype):
     check(c, call(c), c.want())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("P", [16, 32, 128])
+@pytest.mark.parametrize("window,lens,new", [(20, [700, 333], [1, 1]), (50, [900, 161], [6, 4]), (37, [1500, 700], [40, 90]),
+                                             (300, [1500, 700], [1, 200])])
+def test_pages_before_the_window_may_be_given_away(dtype, P, window, lens, new):
+    c = Case(lens, new, H=2, G=4, d=64, P=P, dtype=dtype, seed=window, poison=np.nan)
+    want = c.want(window=window)
+    for b, (n, q) in enumerate(zip(lens, new)):
+        gone = max(0, n - q - window + 1) // P               # pages that no row sees a key of
+        c.table[b, :gone] = -9
+    check(c, call(c, window=window), want)
+
+
+def test_strides_of_single_rows_and_heads_mean_nothing():
+    c = Case([100], [1], H=1, G=1, d=64, P=16, dtype="bf16", seed=3)
+    cache = cache_of(c)
+    q = dev(c.Q, "bf16").as_strided((1, 1, 64), (3, 5, 1))
+    out = torch.empty(64, dtype=torch.bfloat16, device="cuda").as_strided((1, 1, 64), (1, 7, 1))
+    cache.attend(q, dev(c.table), dev(c.lens), dev(c.cu), out=out)
+    O, lse, info = c.want()
+    assert (np.abs(out.double().cpu().numpy() - O) <= bounds(c, info, O, lse)[0]).all()
+    cache.append(q, q, torch.tensor([5], device="cuda"))
+    assert torch.equal(cache.K[0, 0, 5], q[0, 0]) and cache.check_device_error() == 0
+
+
 def test_shared_pages():
     """Two requests whose tables begin with the same pages."""
     c = Case([64, 80], [1, 20], H=2, G=2, d=64, dtype="bf16", seed=12)
@@ -356,6 +381,7 @@ def test_refusals():
                 dict(cu=cu[:1]), dict(table=t.cpu()), dict(slopes=torch.ones(3, device="cuda")),
                 dict(prefix=torch.ones(2, dtype=torch.int32, device="cuda")),
                 dict(first_key=torch.ones(3, dtype=torch.int32, device="cuda")), dict(out=q[:1]),
+                dict(table=t.expand(3, t.shape[1]), lens=lens.expand(3).contiguous(), cu=dev([0, 0, 1, 2])),
                 dict(lse=torch.ones(2, 4, dtype=torch.float16, device="cuda")), dict(Q=q.transpose(1, 2).contiguous().transpose(1, 2))):
         with pytest.raises(ValueError):
             cache.attend(**{**dict(Q=q, table=t, lens=lens, cu=cu), **bad})
