@@ -112,6 +112,10 @@ static size_t lay_work(const Way& w, int D, void* base, Work* out) {
   at = align256(at + (size_t)(w.entries + 1) * sizeof(int64_t));
   const size_t entry = at;
   at = align256(at + (size_t)w.entries * sizeof(Entry));
+  const size_t edge = at;
+  at = align256(at + (size_t)(w.parts + 1) * sizeof(int64_t));
+  const size_t edge_entry = at;
+  at = align256(at + (size_t)(w.parts + 1) * sizeof(int32_t));
   const size_t part = at;
   at = align256(at + (size_t)2 * w.parts * w.rows * (2 + D) * sizeof(float));
   if (out) {
@@ -119,6 +123,8 @@ static size_t lay_work(const Way& w, int D, void* base, Work* out) {
     out->count = reinterpret_cast<int32_t*>(s);
     out->before = reinterpret_cast<int64_t*>(s + before);
     out->entry = reinterpret_cast<Entry*>(s + entry);
+    out->edge = reinterpret_cast<int64_t*>(s + edge);
+    out->edge_entry = reinterpret_cast<int32_t*>(s + edge_entry);
     out->part = reinterpret_cast<float*>(s + part);
     out->parts = w.parts;
   }

@@ -63,20 +63,15 @@ __global__ void __launch_bounds__(kF32Warps * 32) f32_kernel(const F32 f) {
   const uint32_t ring_s = sc::smem_u32(ring);
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  int64_t W = 0, x = 0, x1 = 1;
-  int E0 = 0, N = 1, e = 0;
+  int64_t x = 0, x1 = 1;
+  int e = 0;
   const int part = f.cluster ? (int)(blockIdx.x % f.cluster) : (int)blockIdx.x;
   if (!f.cluster) {
-    E0 = f.w.count[0];
-    W = *reinterpret_cast<const int64_t*>(f.w.count + 2) * a.H;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (W == 0) return;
-    N = parts_used(f.w, W);
-    if (part >= N) return;
-    x = edge<true>(f.w.before, E0, a.H, W, N, part);
-    x1 = edge<true>(f.w.before, E0, a.H, W, N, part + 1);
+    x = f.w.edge[part];
+    x1 = f.w.edge[part + 1];
     if (x >= x1) return;
-    e = entry_of_warp(f.w.before, E0, a.H, x);
+    e = f.w.edge_entry[part];
   }
   const int64_t start = x;
 
@@ -313,15 +308,11 @@ __global__ void __launch_bounds__(kManyWarps * 32, 2) f32_many_kernel(const F32 
   const uint32_t base = sc::smem_u32(smem);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int E0 = f.w.count[0], part = blockIdx.x;
-  const int64_t W = *reinterpret_cast<const int64_t*>(f.w.count + 2) * a.H;
-  if (W == 0) return;
-  const int N = parts_used(f.w, W);
-  if (part >= N) return;
-  const int64_t start = edge<true>(f.w.before, E0, a.H, W, N, part), x1 = edge<true>(f.w.before, E0, a.H, W, N, part + 1);
+  const int part = blockIdx.x;
+  const int64_t start = f.w.edge[part], x1 = f.w.edge[part + 1];
   int64_t x = start;
   if (x >= x1) return;
-  int e = entry_of_warp(f.w.before, E0, a.H, x);
+  int e = f.w.edge_entry[part];
 
   while (x < x1) {
     while (f.w.before[e + 1] * a.H <= x) ++e;
@@ -577,7 +568,7 @@ cudaError_t attend_f32(const Attend& a, const mp_paged_cache& c, const Work& w, 
   if (rows == kF32ManyRows) e = D == 128 ? launch_many<128>(f, st) : launch_many<64>(f, st);
   else e = D == 128 ? launch_f32<128>(f, rows, units, st) : launch_f32<64>(f, rows, units, st);
   if (e != cudaSuccess || cluster) return e;
-  return launch_join(a, w, MP_F32, D, tile, rows, st);
+  return launch_join(a, w, MP_F32, D, tile, rows, false, st);
 }
 
 }  // namespace paged

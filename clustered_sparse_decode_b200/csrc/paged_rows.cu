@@ -183,10 +183,10 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) few_kernel(const __grid_con
     if (W == 0) return;
     N = parts_used(f.w, W);
     if (part >= N) return;
-    x = edge<false>(before, E, a.H, W, N, part);
-    x1 = edge<false>(before, E, a.H, W, N, part + 1);
+    x = own ? edge(before, E, a.H, W, N, part) : f.w.edge[part];
+    x1 = own ? edge(before, E, a.H, W, N, part + 1) : f.w.edge[part + 1];
     if (x >= x1) return;
-    e = entry_of(before, E, a.H, x);
+    e = own ? entry_of(before, E, a.H, x) : f.w.edge_entry[part];
   } else {
     x1 = 1;
   }
@@ -517,7 +517,7 @@ cudaError_t attend_few(const Attend& a, const mp_paged_cache& c, Work w, int cel
   f.w = w;
   cudaError_t e = a.batch > kOwnList ? launch_work(a, w, a.max_new, kFewBlock, st) : cudaSuccess;
   if (e == cudaSuccess) e = launch_few(f, c.cfg.dtype, D, cells, a.batch * a.H, st);
-  if (e == cudaSuccess) e = launch_join(a, w, c.cfg.dtype, D, a.max_new, few_rows(cells), st);
+  if (e == cudaSuccess) e = launch_join(a, w, c.cfg.dtype, D, a.max_new, few_rows(cells), a.batch <= kOwnList, st);
   return e;
 }
 

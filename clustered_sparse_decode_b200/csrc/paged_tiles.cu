@@ -783,15 +783,10 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
       // otherwise lie between two items of each.
       uint32_t n_kv = 0, n_q = 0, issued = 0;
       const int pg = 1 << a.page_shift, boxes = kKeys / f.box;
-      const int E = f.w.count[0];
-      const int64_t W = *reinterpret_cast<const int64_t*>(f.w.count + 2) * a.H;
-      const int N = W > 0 ? parts_used(f.w, W) : 0;
-      Walk walk{0, 0, 0, 0};
-      if (part < N) {
-        walk.x = walk.start = edge<true>(f.w.before, E, a.H, W, N, part);
-        walk.x1 = edge<true>(f.w.before, E, a.H, W, N, part + 1);
-        if (walk.x < walk.x1) walk.e = entry_of_warp(f.w.before, E, a.H, walk.x);
-      }
+      Walk walk;
+      walk.x = walk.start = f.w.edge[part];
+      walk.x1 = f.w.edge[part + 1];
+      walk.e = f.w.edge_entry[part];
       uint32_t n_item = 0;
       auto publish = [&](Item& x) {                      // finds the next item and hands it on
         const uint32_t slot = n_item % kItems;
@@ -923,7 +918,7 @@ cudaError_t attend_tiles(const Attend& a, const mp_paged_cache& c, const Work& w
   if (c.cfg.dtype == MP_F16) e = D == 128 ? launch_tiles<__half, 128>(f, st) : launch_tiles<__half, 64>(f, st);
   else e = D == 128 ? launch_tiles<__nv_bfloat16, 128>(f, st) : launch_tiles<__nv_bfloat16, 64>(f, st);
   if (e != cudaSuccess) return e;
-  return launch_join(a, w, c.cfg.dtype, D, f.tile, 2 * kHalf, st);
+  return launch_join(a, w, c.cfg.dtype, D, f.tile, 2 * kHalf, false, st);
 }
 
 }  // namespace paged

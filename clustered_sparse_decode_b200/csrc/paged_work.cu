@@ -17,6 +17,7 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const Attend a, cons
   __shared__ int64_t sums[2][32];
   __shared__ int32_t first[kListThreads + 1];            // entries before each request of the round
   __shared__ int32_t spans[2][kListThreads];             // of the round's entries: first key, blocks (first_key only)
+  __shared__ int64_t sums_of[kListThreads + 1];          // w.before, if it is short
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int turn = 0;
   // exclusive sum of x over the block's threads, and their total; consecutive calls use different halves of `sums`
@@ -99,6 +100,7 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const Attend a, cons
       if (e0 + tid < round) {
         w.entry[entries + e0 + tid] = x;
         w.before[entries + e0 + tid] = blocks + before;
+        if (entries + e0 + tid < kListThreads) sums_of[entries + e0 + tid] = blocks + before;
       }
       blocks += cost;
       if (a.first_key) __syncthreads();                  // spans are read
@@ -110,6 +112,17 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const Attend a, cons
     w.before[entries] = blocks;
     w.count[0] = (int32_t)entries;
     *reinterpret_cast<int64_t*>(w.count + 2) = blocks;
+    if (entries <= kListThreads) sums_of[entries] = blocks;
+  }
+  __syncthreads();
+  // where the parts begin, found here once (a dozen dependent loads in each of their blocks otherwise)
+  const int64_t W = blocks * a.H;
+  const int E = (int)entries, N = W > 0 ? parts_used(w, W) : 0;
+  const int64_t* before = entries <= kListThreads ? sums_of : w.before;
+  for (int c = tid; c <= w.parts; c += kListThreads) {
+    const int64_t x = c < N ? edge(before, E, a.H, W, N, c) : W;
+    w.edge[c] = x;
+    w.edge_entry[c] = x < W ? entry_of(before, E, a.H, x) : 0;
   }
 }
 
@@ -122,7 +135,7 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const Attend a, cons
 constexpr int kJoinWarps = 4;
 
 template <typename T, int D, int R>
-__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Attend a, const Work w, int tile, int rows) {
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Attend a, const Work w, int tile, int rows, int own) {
   constexpr int E = D / 32;                    // columns a lane
   using Vec = typename std::conditional<E == 4, float4, float2>::type;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -139,7 +152,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Attend a, c
   const int64_t u0 = first + h * n, u1 = u0 + n;
   // an edge between units, of a unit that is not cut, or not the first inside its unit
   if (x == u0 || n <= kWholeBlocks || share(W, N, c - 1) > u0) return;
-  const int64_t before = edge<true>(w.before, count, a.H, W, N, c - 1);
+  const int64_t before = own ? edge(w.before, count, a.H, W, N, c - 1) : w.edge[c - 1];
   const int c1 = part_of(W, N, u1 - 1), np = c1 - c + 2;
   const Request r = request_of(a, en.b);
   const int cells = min(tile, r.n - en.tile * tile) * a.G, lane = threadIdx.x & 31;
@@ -210,7 +223,8 @@ cudaError_t launch_work(const Attend& a, const Work& w, int tile, int block, cud
 }
 
 template <int R>
-static cudaError_t launch_join_r(const Attend& a, const Work& w, int dtype, int D, int tile, int rows, cudaStream_t st) {
+static cudaError_t launch_join_r(const Attend& a, const Work& w, int dtype, int D, int tile, int rows, int own,
+                                 cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(w.parts - 1), (unsigned)((rows + kJoinWarps * R - 1) / (kJoinWarps * R)));
   cfg.blockDim = dim3(kJoinWarps * 32);
@@ -220,15 +234,16 @@ static cudaError_t launch_join_r(const Attend& a, const Work& w, int dtype, int 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  auto go = [&](auto kernel) { return cudaLaunchKernelEx(&cfg, kernel, a, w, tile, rows); };
+  auto go = [&](auto kernel) { return cudaLaunchKernelEx(&cfg, kernel, a, w, tile, rows, own); };
   if (dtype == MP_F32) return D == 128 ? go(join_kernel<float, 128, R>) : go(join_kernel<float, 64, R>);
   if (dtype == MP_F16) return D == 128 ? go(join_kernel<__half, 128, R>) : go(join_kernel<__half, 64, R>);
   return D == 128 ? go(join_kernel<__nv_bfloat16, 128, R>) : go(join_kernel<__nv_bfloat16, 64, R>);
 }
 
-cudaError_t launch_join(const Attend& a, const Work& w, int dtype, int D, int tile, int rows, cudaStream_t st) {
+cudaError_t launch_join(const Attend& a, const Work& w, int dtype, int D, int tile, int rows, bool own, cudaStream_t st) {
   if (w.parts < 2) return cudaSuccess;
-  return rows <= 32 ? launch_join_r<1>(a, w, dtype, D, tile, rows, st) : launch_join_r<4>(a, w, dtype, D, tile, rows, st);
+  return rows <= 32 ? launch_join_r<1>(a, w, dtype, D, tile, rows, own, st)
+                    : launch_join_r<4>(a, w, dtype, D, tile, rows, own, st);
 }
 
 }  // namespace paged

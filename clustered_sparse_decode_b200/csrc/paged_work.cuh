@@ -29,6 +29,8 @@ struct Work {
   int32_t* count;                    // entries; 8 bytes on, as 64 bits: blocks of all, for one head
   int64_t* before;                   // [entries + 1] blocks of the entries before, for one head
   Entry* entry;                      // [entries]
+  int64_t* edge;                     // [parts + 1] where each part begins (the list kernel's)
+  int32_t* edge_entry;               // [parts + 1] and in which entry
   float* part;                       // [2 parts][rows (2 + D)]: maxima, sums, numerators
   int32_t parts;                     // parts launched
   int32_t least;                     // blocks a part gets at least, as far as there are that many
@@ -169,12 +171,11 @@ __device__ void settle(const Attend& a, const Settle& s, const float* ml, float*
   cl.sync();                           // no block leaves while its state is read
 }
 
-// where part c begins: by a thread, or by the lanes of a warp together
-template <bool WARP>
+// where part c begins
 __device__ __forceinline__ int64_t edge(const int64_t* before, int E, int H, int64_t W, int N, int c) {
   const int64_t x = share(W, N, c);
   if (x <= 0 || x >= W) return x;
-  const int e = WARP ? entry_of_warp(before, E, H, x) : entry_of(before, E, H, x);
+  const int e = entry_of(before, E, H, x);
   const int64_t n = before[e + 1] - before[e];
   if (n > kWholeBlocks) return x;
   const int64_t in = (x - before[e] * H) % n;
@@ -184,7 +185,8 @@ __device__ __forceinline__ int64_t edge(const int64_t* before, int E, int H, int
 // Makes the list: tiles of `tile` rows (tokens), blocks of `block` keys.
 cudaError_t launch_work(const Attend& a, const Work& w, int tile, int block, cudaStream_t st);
 // Joins the partial results of cut units: `rows` (token, head) rows a unit, of `tile` tokens.
-cudaError_t launch_join(const Attend& a, const Work& w, int dtype, int D, int tile, int rows, cudaStream_t st);
+// own: the parts' blocks made the list, not the list kernel.
+cudaError_t launch_join(const Attend& a, const Work& w, int dtype, int D, int tile, int rows, bool own, cudaStream_t st);
 
 // Few rows (paged_rows.cu): `cells` (token, head) rows a unit at most.  cluster
 // > 0: that many blocks share a unit and no list or scratch is needed.
