@@ -95,15 +95,15 @@ def attend_args(**kw):
 ])
 def test_attend_refusals(lib, kw, status):
     h, need = cache(), ctypes.c_size_t()
-    assert lib.mp_paged_attend_scratch(ctypes.addressof(h), attend_args(**kw), ctypes.byref(need)) == status
+    assert lib.mp_paged_attend_scratch(ctypes.byref(h), attend_args(**kw), ctypes.byref(need)) == status
     if status != L.MP_OK:
-        assert lib.mp_paged_attend(ctypes.addressof(h), attend_args(**kw), None, 0, None) == status
+        assert lib.mp_paged_attend(ctypes.byref(h), attend_args(**kw), None, 0, None) == status
 
 
 def test_scratch_is_asked_for_where_keys_are_shared_out(lib):
     def need(dtype=L.MP_BF16, **kw):
         n = ctypes.c_size_t()
-        assert lib.mp_paged_attend_scratch(ctypes.addressof(cache(dtype)), attend_args(**kw), ctypes.byref(n)) == L.MP_OK
+        assert lib.mp_paged_attend_scratch(ctypes.byref(cache(dtype)), attend_args(**kw), ctypes.byref(n)) == L.MP_OK
         return n.value
     long = dict(table_pages=1 << 16, table_stride=1 << 16)
     assert need() == 0 and need(L.MP_F32) == 0 and need(rows=0, max_new=0) == 0 and need(batch=0) == 0
@@ -124,7 +124,7 @@ def test_plan_refusals(lib, kw):
             setattr(a, f, FAKE)
     for k, v in kw.items():
         setattr(a, k, v)
-    assert lib.mp_paged_plan(ctypes.addressof(cache()), bytes(a), None) == L.MP_EINVAL
+    assert lib.mp_paged_plan(ctypes.byref(cache()), bytes(a), None) == L.MP_EINVAL
 
 
 def test_plan_of_too_many_requests(lib):
@@ -132,11 +132,11 @@ def test_plan_of_too_many_requests(lib):
     for f, t in L.MpPagedPlanArgs._fields_:
         if t is ctypes.c_void_p:
             setattr(a, f, FAKE)
-    assert lib.mp_paged_plan(ctypes.addressof(cache()), bytes(a), None) == L.MP_EUNSUPPORTED
+    assert lib.mp_paged_plan(ctypes.byref(cache()), bytes(a), None) == L.MP_EUNSUPPORTED
 
 
 def test_append_and_gather_refusals(lib):
-    h = ctypes.addressof(cache())
+    h = ctypes.byref(cache())                        # byref holds the cache, its bare address would not
     for args in ((FAKE, FAKE, 128, 64, FAKE, -1), (None, FAKE, 128, 64, FAKE, 2), (FAKE, None, 128, 64, FAKE, 2),
                  (FAKE, FAKE, 128, 64, None, 2), (FAKE + 2, FAKE, 128, 64, FAKE, 2), (FAKE, FAKE, 124, 64, FAKE, 2),
                  (FAKE, FAKE, 128, 4, FAKE, 2), (FAKE, FAKE, -128, 64, FAKE, 2)):
