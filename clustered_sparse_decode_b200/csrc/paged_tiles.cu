@@ -334,7 +334,7 @@ __device__ __forceinline__ float2 exp2_pair(float2 x) {
 __device__ constexpr float kTanh[6] = {1.0f, -0.33332958817481995f, 0.1332540661096573f, -0.05334442853927612f,
                                        0.01958290860056877f, -0.004716257099062204f};
 // The same on |u| <= 5/16, 2^-26: two terms fewer (odd chunks and decode
-// tokens, scores capped at 30 over a window: 191 us -> 180 us; where every |u|
+// tokens, scores capped at 30 over a window: 191 us -> 179 us; where every |u|
 // passes 3/4, the extra look costs 199 us -> 202 us).
 __device__ constexpr float kTanhNear[4] = {1.0f, -0.33332863450050354f, 0.1330905258655548f, -0.04992058873176575f};
 template <int N>
@@ -575,10 +575,10 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
             if (a.cap > 0.f) {
               // cap tanh(u), u = z / cap: by its exponential (two results of a unit that the weights need too) only
               // where some |u| of the warp's 32 columns is above 3/4
-              float far = 0.f;
+              float t[4] = {};
 #pragma unroll
-              for (int q = 0; q < 32; q += 2) far = max3(far, fabsf(z[q]), fabsf(z[q + 1]));
-              far *= fabsf(to_u);
+              for (int q = 0; q < 32; q += 2) t[q / 2 & 3] = max3(t[q / 2 & 3], fabsf(z[q]), fabsf(z[q + 1]));
+              const float far = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * fabsf(to_u);
               if (__all_sync(kFull, far <= fminf(most, 0.3125f))) {
 #pragma unroll
                 for (int q = 0; q < 32; q += 2) {
