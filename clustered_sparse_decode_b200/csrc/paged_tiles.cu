@@ -301,30 +301,24 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
       : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
   return d;
 }
-// 2^x for x <= 128 by arithmetic: x = n + f with n the nearest integer (what
-// adding 1.5 * 2^23 leaves in the low bits) and |f| <= 1/2, 2^f by a polynomial
-// whose relative error is least on that interval (Remez exchange): 7.5e-5 of
-// degree 3 for bf16 weights, whose rounding is off by up to 3.9e-3 / 2; 2.6e-6 of
-// degree 4 for fp16's 4.9e-4 / 2.  Below -126.5, minus infinity included, the
-// result is 0; a NaN stays one.
-template <typename T>
+// 2^x for x <= 127 by arithmetic: x = n + f with n the nearest integer (what
+// adding 1.5 * 2^23 leaves in the low bits) and |f| <= 1/2, 2^f by the polynomial
+// of degree 5 whose relative error is least on that interval (Remez exchange),
+// 2^-22 with its roundings: the weights enter the row's sum, and with it the lse,
+// before they are rounded to the values' type, so they are as good as the
+// exponential unit's whatever that type is.  Below -126.5, minus infinity
+// included, the result is 0; a NaN stays one.
 __device__ __forceinline__ float2 exp2_pair(float2 x) {
   asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x.x));   // -127
   asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x.y));
   const float2 magic = make_float2(12582912.f, 12582912.f), back = make_float2(-12582912.f, -12582912.f);
   const float2 r = add2(x, magic), f = fma2(add2(r, back), make_float2(-1.f, -1.f), x);
   auto c = [](float v) { return make_float2(v, v); };
-  float2 p;
-  if constexpr (std::is_same<T, __half>::value) {
-    p = fma2(c(0.009570102207362652f), f, c(0.05591785907745361f));
-    p = fma2(p, f, c(0.240247443318367f));
-    p = fma2(p, f, c(0.6931217908859253f));
-    p = fma2(p, f, c(0.9999992847442627f));
-  } else {
-    p = fma2(c(0.0551716685295105f), f, c(0.2426111251115799f));
-    p = fma2(p, f, c(0.6932609677314758f));
-    p = fma2(p, f, c(0.9999280571937561f));
-  }
+  float2 p = fma2(c(0.0013276472454890609f), f, c(0.009675540961325169f));
+  p = fma2(p, f, c(0.05550713092088699f));
+  p = fma2(p, f, c(0.24022120237350464f));
+  p = fma2(p, f, c(0.6931469440460205f));
+  p = fma2(p, f, c(1.0000001192092896f));
   const float2 scale = make_float2(__int_as_float((__float_as_int(r.x) << 23) + 0x3f800000),
                                    __int_as_float((__float_as_int(r.y) << 23) + 0x3f800000));
   return mul2(p, scale);
@@ -526,7 +520,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
             const float2 x = fma2(make_float2(z[2 * q], z[2 * q + 1]), mul, sub);
             // every fourth pair by arithmetic: the exponential unit alone needs 1024 cycles a half, as long as the
             // products (none: 745 us for 4K tokens over 12K, two of eight in a row 731, every fourth 721, three 745)
-            const float2 w = (q & 3) == 3 ? exp2_pair<T>(x) : make_float2(sc::ex2(x.x), sc::ex2(x.y));
+            const float2 w = (q & 3) == 3 ? exp2_pair(x) : make_float2(sc::ex2(x.x), sc::ex2(x.y));
             sum[q & 1] = add2(sum[q & 1], w);
             p[q] = to_pair<T>(w.x, w.y);
           }

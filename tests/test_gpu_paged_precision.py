@@ -1,0 +1,41 @@
+"""Paged attention where rounding could go wrong, against 64-bit results of the same inputs; tolerances count roundings."""
+import numpy as np
+import pytest
+
+from paged_cases import Case, call
+
+pytestmark = pytest.mark.gpu
+
+
+def line_case(n, new, G, dtype, q, k):
+    """Scores are single exact products: row r has q[r] in its first element, key j k[j]."""
+    c = Case([n], [new], H=1, G=G, d=64, P=64, dtype=dtype, seed=1)
+    c.Q[:] = 0.0
+    c.Q[:, :, 0] = np.asarray(q)[:, None]
+    j = np.arange(n)
+    c.K[:] = 0.0
+    page, row = c.at(0, j)
+    c.K[page, 0, row, 0] = k
+    return c
+
+
+def line_lse_tol(n, info, lse):
+    """A score: one exact product, then scaling, base 2 and the maximum's subtraction, 4 roundings of at most zmax.
+    A weight's exponential: 2^-21.  A sum of n weights by at least 4 chains: n / 4 roundings.  The logarithm, its
+    sum with the maximum and the change of base: 8 roundings of 1 + |lse|."""
+    return 2.0 ** -22 * info["zmax"] + 2.0 ** -21 + n / 4 * 2.0 ** -24 + 8 * 2.0 ** -24 * (1 + np.abs(lse))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("G,new", [(1, 1), (4, 4), (8, 4), (1, 64), (4, 40)])
+@pytest.mark.parametrize("kind", ["equal", "one_in_four", "spread"])
+def test_lse_counts_every_weight_in_32_bits(dtype, G, new, kind):
+    n = 256
+    j = np.arange(n)
+    k = {"equal": np.zeros(n), "one_in_four": np.where(j % 8 >= 6, 0.0, -2048.0), "spread": (j * 37 % 64) / 64.0 - 0.5}[kind]
+    c = line_case(n, new, G, dtype, 1.0 + (np.arange(new) % 8) / 8, k)
+    got = call(c, scale=1.0, full=True)
+    O, lse, info = c.want(scale=1.0, full=True)
+    # keys whose weight is 0 do not move the sum, whatever their score
+    zmax = {k: (np.minimum(v, 1.0) if k == "zmax" else v) for k, v in info.items()}
+    assert (np.abs(got[1] - lse) <= line_lse_tol(n, zmax, lse)).all(), np.abs(got[1] - lse).max()
