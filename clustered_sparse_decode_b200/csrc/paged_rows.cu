@@ -17,10 +17,11 @@
 // with 16 keys as K), so the P that comes out of S is already the operand that
 // P V takes.  With at most 8 rows the other 8 are the same rows again, whose
 // lanes pass the remainder p - round(p) into P V: the weights keep twice the
-// type's bits at no cost.  Above that, weights are rounded once to the values'
-// type.  The running maximum is lazy: it moves when a score exceeds it by more
-// than 8 (base 2), so weights stay below 256 and the numerator is rarely
-// rescaled.  Statistics and numerators are fp32.
+// type's bits at no cost (fp16's down to its smallest step).  Above that, weights
+// are rounded once to the values' type, off by at most half a step each, as the
+// matrix instruction has no operand of more bits.  The running maximum is lazy: it
+// moves when a score exceeds it by more than 8 (base 2), so weights stay below 256
+// and the numerator is rarely rescaled.  Statistics and numerators are fp32.
 #include <cstring>
 #include <type_traits>
 
@@ -388,7 +389,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) few_kernel(const __grid_con
 #pragma unroll
           for (int hrow = 0; hrow < 2; ++hrow) {
             if (DUP && hrow == 1) continue;
-            const float base = m[mt][hrow] == -INFINITY ? 0.f : m[mt][hrow];
+            const float base = m[mt][hrow] == -INFINITY ? 0.f : m[mt][hrow] - kLift<T>;
 #pragma unroll
             for (int nh = 0; nh < 2; ++nh) {
               const float p0 = sc::ex2(z[mt][nh][2 * hrow] - base), p1 = sc::ex2(z[mt][nh][2 * hrow + 1] - base);
@@ -436,7 +437,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) few_kernel(const __grid_con
         s += __shfl_xor_sync(kFull, s, 2);
         const int row = mt * 16 + hrow * 8 + g;
         if (t4 == 0) {
-          ml[(warp * 2) * ROWS + row] = s != s ? s : m[mt][hrow];      // a NaN must not pass for "nothing seen"
+          ml[(warp * 2) * ROWS + row] = s != s ? s : m[mt][hrow] - kLift<T>;   // a NaN must not pass for "nothing seen"
           ml[(warp * 2 + 1) * ROWS + row] = s;
         }
 #pragma unroll

@@ -188,6 +188,16 @@ cudaError_t launch_work(const Attend& a, const Work& w, int tile, int block, cud
 // own: the parts' blocks made the list, not the list kernel.
 cudaError_t launch_join(const Attend& a, const Work& w, int dtype, int D, int tile, int rows, bool own, cudaStream_t st);
 
+// Weights that a product takes in the values' type are 2^(z - m + kLift): fp16's
+// smallest step is 2^-24, so that of 64K keys whose weights lie just below half of
+// it all would vanish from the numerator (0.2% of the largest weight together) and
+// stay in the sum.  7 lifts the largest, 2^8 by the lazy maximum, to 2^15 of
+// fp16's 65504, and what rounding can lose of a weight to 2^-32 of the largest.
+// bf16 has fp32's range.  A state's maximum is then m - kLift, which its sum and
+// numerator count from.
+template <typename T> constexpr float kLift = 0.f;
+template <> constexpr float kLift<__half> = 7.f;
+
 // Few rows (paged_rows.cu): `cells` (token, head) rows a unit at most.  cluster
 // > 0: that many blocks share a unit and no list or scratch is needed.
 constexpr int kFewBlock = 64;                      // keys a block of the share-out

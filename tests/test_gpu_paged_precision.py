@@ -2,7 +2,7 @@
 import numpy as np
 import pytest
 
-from paged_cases import Case, call
+from paged_cases import Case, U, call
 
 pytestmark = pytest.mark.gpu
 
@@ -39,3 +39,29 @@ def test_lse_counts_every_weight_in_32_bits(dtype, G, new, kind):
     # keys whose weight is 0 do not move the sum, whatever their score
     zmax = {k: (np.minimum(v, 1.0) if k == "zmax" else v) for k, v in info.items()}
     assert (np.abs(got[1] - lse) <= line_lse_tol(n, zmax, lse)).all(), np.abs(got[1] - lse).max()
+
+
+@pytest.mark.parametrize("G,new", [(1, 1), (4, 3), (8, 3), (1, 20), (1, 64)])
+def test_many_small_fp16_weights_add_up(G, new):
+    """One key far above 60,000 others, each of whose weights is below half of fp16's smallest step.
+
+    Requests of the same pages, so many that no request's keys are shared out: each keeps one maximum.  A weight's
+    rounding is off by at most 2^-25 of 2^7 (the largest weight's place), so n of them by n 2^-32 of the values; the
+    exponentials and sums add 2^-19, the output's rounding 2^-11 of it.  The sum beside the lone key is a chain in 32
+    bits: a lane adds pairs of weights, a pair in 32 keys, each sum rounded to 2^-24 of it.
+    """
+    n, B = 60000, 296
+    k = np.full(n, -17.5)
+    k[123] = 0.0
+    c = line_case(n, new, G, "f16", np.ones(new), k)
+    c.V[:] = 1.0
+    page, row = c.at(0, 123)
+    c.V[page, :, row] = 0.0
+    O, lse, _ = c.want(scale=1.0)
+    assert O.min() > 1e-3
+    c.table, c.Q = np.repeat(c.table, B, 0), np.tile(c.Q, (B, 1, 1))
+    c.lens, c.new, c.cu, c.rows = [n] * B, [new] * B, np.arange(B + 1) * new, B * new
+    got, gl = call(c, scale=1.0)
+    off = np.abs(got.reshape(B, new, G, 64) - O)
+    assert (off <= n * 2.0 ** -32 + 2.0 ** -19 * O + U["f16"] * O + 2.0 ** -25).all(), off.max()
+    assert np.abs(gl.reshape(B, new, G) - lse).max() <= n / 32 * 2.0 ** -24 + 2.0 ** -22 * 17.5 + 2.0 ** -19
