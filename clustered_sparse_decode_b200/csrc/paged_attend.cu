@@ -45,6 +45,10 @@ static Attend args_of(const mp_paged_cache& c, const mp_paged_attend_args& p) {
   if (p.q_heads == 1) a.q_head_b = a.o_head_b = row;
   a.scale = p.scale != 0.f ? p.scale : 1.f / sqrtf((float)g.head_dim);
   a.cap = p.softcap;
+  a.to_z = a.scale * kLog2e;
+  const float huge = 0x1p126f;         // for caps and ratios that fp32 cannot hold: 0 times them stays 0
+  a.to_u = a.cap > 0.f ? std::min(std::max(a.scale / a.cap, -huge), huge) : 0.f;
+  a.cap2 = std::min(a.cap * kLog2e, huge);
   a.window = std::min(p.window, 1 << 30);
   a.full = (p.flags & MP_ATTEND_FULL) != 0;
   a.slopes = p.slopes;

@@ -33,8 +33,9 @@ struct Attend {
   const char* Q;
   char* O;
   int64_t q_row_b, q_head_b, o_row_b, o_head_b;
-  float scale;                         // of q.k; its value in the exponent's base 2 is scale * log2 e
+  float scale;                         // of q.k
   float cap;                           // 0: none
+  float to_z, to_u, cap2;              // scale in the exponent's base 2; scale / cap; cap in base 2
   int32_t window;                      // 0: none, at most 2^30
   int32_t full;
   const float* slopes;

@@ -76,11 +76,6 @@ __device__ __forceinline__ void tma_5d(uint32_t dst, const CUtensorMap* tm, int 
       "%5}], [%6];\n" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tm)), "r"(0), "r"(row), "r"(head), "r"(page), "r"(bar)
       : "memory");
 }
-// tanh through the exponential unit: 1 - 2 / (1 + e^2x), off by a few 2^-24 of 1
-__device__ __forceinline__ float tanh_fast(float x) {
-  return 1.f - __fdividef(2.f, 1.f + sc::ex2(2.f * kLog2e * x));
-}
-
 // Waits for a phase, two seconds at most.
 __device__ __forceinline__ bool wait_limited(uint32_t bar, uint32_t parity) {
   return sc::mbar_try(bar, parity) || sc::mbar_wait(bar, parity, sc::gtimer() + 2000000000LL);
@@ -354,10 +349,8 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) few_kernel(const __grid_con
           for (int nh = 0; nh < 2; ++nh)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              float v = z[mt][nh][c];
+              float v = a.cap > 0.f ? cap_of(a, z[mt][nh][c]) : z[mt][nh][c] * a.to_z;
               const int j = j0 + nh * 8 + 2 * t4 + (c & 1), hrow = c >> 1;
-              if (a.cap > 0.f) v = a.cap * kLog2e * tanh_fast(v * (a.scale / a.cap));
-              else v *= a.scale * kLog2e;
               if (a.slopes) v -= slope[mt][hrow] * (float)abs(pos[mt][hrow] - j);
               if (!whole && (j < lo[mt][hrow] || j >= hi[mt][hrow])) v = -INFINITY;
               z[mt][nh][c] = v;

@@ -292,11 +292,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-__device__ __forceinline__ float rcp(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   float2 d;
   asm("mul.rn.f32x2 %0, %1, %2;"
@@ -326,11 +321,7 @@ __device__ __forceinline__ float2 exp2_pair(float2 x) {
                                    __int_as_float((__float_as_int(r.y) << 23) + 0x3f800000));
   return mul2(p, scale);
 }
-// tanh(u) / u = sum of kTanh[i] u^(2 i) on |u| <= 3/4: the polynomial of its
-// degree with the least relative error there, 2^-25 (Remez exchange).
-__device__ constexpr float kTanh[6] = {1.0f, -0.33332958817481995f, 0.1332540661096573f, -0.05334442853927612f,
-                                       0.01958290860056877f, -0.004716257099062204f};
-// The same on |u| <= 5/16, 2^-26: two terms fewer (odd chunks and decode
+// kTanh's like on |u| <= 5/16, 2^-26: two terms fewer (odd chunks and decode
 // tokens, scores capped at 30 over a window: 191 us -> 179 us; where every |u|
 // passes 3/4, the extra look costs 199 us -> 202 us).
 __device__ constexpr float kTanhNear[4] = {1.0f, -0.33332863450050354f, 0.1330905258655548f, -0.04992058873176575f};
@@ -451,20 +442,19 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
     const int g = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t tS = tmem + 128 * g + lanes, tO = tmem + 256 + 128 * g + lanes;
-    const float c = a.scale * kLog2e;
-    // cap tanh(u), u = s scale / cap, in base 2: cap - 2 cap / (1 + e^(2 u)), or s times a polynomial of s^2
-    const float cap2 = a.cap * kLog2e, cap_in = GEN && a.cap > 0.f ? 2.f * c / a.cap : 0.f,
-                to_u = GEN && a.cap > 0.f ? a.scale / a.cap : 0.f;
+    const float c = a.to_z;
+    // capped scores as s times a polynomial of s^2 (cap_of's), its coefficients made for the raw score, while no s^2 and
+    // no coefficient passes fp32's range; cap_of otherwise
     float capped[6], near[4];
     {
-      float f = cap2 * to_u;
+      float f = a.to_z;
 #pragma unroll
-      for (int q = 0; q < 6; ++q, f *= to_u * to_u) {
+      for (int q = 0; q < 6; ++q, f *= a.to_u * a.to_u) {
         capped[q] = kTanh[q] * f;
         if (q < 4) near[q] = kTanhNear[q] * f;
       }
     }
-    const float most = isfinite(capped[5]) ? 0.75f : -1.f;    // the |u| that the polynomial is for (a tiny cap: none)
+    const float most = isfinite(capped[5]) ? kTanhMost : -1.f;
     const bool straight = !a.full && !a.prefix;          // no row sees a key behind its own
     uint32_t n_s = 0, n_o = 0, n_kv = 0;                 // phases of s_full and o_full, tiles that have passed the ring
     for (uint32_t n_item = 0; take(n_item); ++n_item) {
@@ -570,12 +560,12 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
             tmem_ld(tS + 32 * k, z);
             tmem_ld_wait(z);
             if (a.cap > 0.f) {
-              // cap tanh(u), u = z / cap: by its exponential (two results of a unit that the weights need too) only
-              // where some |u| of the warp's 32 columns is above 3/4
+              // the exponential (two results of a unit that the weights need too) only where some |u| of the warp's 32
+              // columns is above 3/4
               float t[4] = {};
 #pragma unroll
               for (int q = 0; q < 32; q += 2) t[q / 2 & 3] = max3(t[q / 2 & 3], fabsf(z[q]), fabsf(z[q + 1]));
-              const float far = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * fabsf(to_u);
+              const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), far = top <= 0x1p60f ? top * fabsf(a.to_u) : 1.f;
               if (__all_sync(kFull, far <= fminf(most, 0.3125f))) {
 #pragma unroll
                 for (int q = 0; q < 32; q += 2) {
@@ -589,7 +579,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
                 }
               } else if (__any_sync(kFull, far > most)) {
 #pragma unroll
-                for (int q = 0; q < 32; ++q) z[q] = fmaf(-2.f * cap2, rcp(1.f + sc::ex2(z[q] * cap_in)), cap2);
+                for (int q = 0; q < 32; ++q) z[q] = cap_of(a, z[q]);
               } else {
 #pragma unroll
                 for (int q = 0; q < 32; q += 2) {

@@ -17,6 +17,7 @@
 #include <atomic>
 
 #include "paged_common.cuh"
+#include "stream_common.cuh"
 
 namespace mp {
 namespace paged {
@@ -187,6 +188,35 @@ cudaError_t launch_work(const Attend& a, const Work& w, int tile, int block, cud
 // Joins the partial results of cut units: `rows` (token, head) rows a unit, of `tile` tokens.
 // own: the parts' blocks made the list, not the list kernel.
 cudaError_t launch_join(const Attend& a, const Work& w, int dtype, int D, int tile, int rows, bool own, cudaStream_t st);
+
+// The cap of scores, cap tanh(u) with u = scale q.k / cap, in the exponent's base
+// 2.  Up to |u| = 3/4 it is the score times a polynomial of u^2, above that
+// cap - 2 cap / (1 + e^(2 u)): that form is off by a few 2^-24 of the cap, far too
+// much where the score is far below it.
+//
+// tanh(u) / u = sum of kTanh[i] u^(2 i) on |u| <= 3/4: the polynomial of its
+// degree with the least relative error there, 2^-25 (Remez exchange).
+__device__ constexpr float kTanh[6] = {1.0f, -0.33332958817481995f, 0.1332540661096573f, -0.05334442853927612f,
+                                       0.01958290860056877f, -0.004716257099062204f};
+constexpr float kTanhMost = 0.75f;
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// both forms and a selection: as a branch, rows' scores on both sides of 3/4 took twice the time
+__device__ __forceinline__ float cap_of(const Attend& a, float z) {
+  const float u = z * a.to_u, x = u * u;
+  float y = kTanh[5];
+#pragma unroll
+  for (int q = 4; q >= 0; --q) y = fmaf(y, x, kTanh[q]);
+  const float near = z * a.to_z * y, far = fmaf(-2.f * a.cap2, rcp(1.f + sc::ex2(u * (2.f * kLog2e))), a.cap2);
+  float r;
+  asm("{\n .reg .pred p;\n setp.le.f32 p, %1, %2;\n selp.f32 %0, %3, %4, p;\n}\n"
+      : "=f"(r)
+      : "f"(fabsf(u)), "f"(kTanhMost), "f"(near), "f"(far));
+  return r;
+}
 
 // Weights that a product takes in the values' type are 2^(z - m + kLift): fp16's
 // smallest step is 2^-24, so that of 64K keys whose weights lie just below half of

@@ -2,7 +2,7 @@
 import numpy as np
 import pytest
 
-from paged_cases import Case, U, call
+from paged_cases import Case, U, call, check
 
 pytestmark = pytest.mark.gpu
 
@@ -65,3 +65,29 @@ def test_many_small_fp16_weights_add_up(G, new):
     off = np.abs(got.reshape(B, new, G, 64) - O)
     assert (off <= n * 2.0 ** -32 + 2.0 ** -19 * O + U["f16"] * O + 2.0 ** -25).all(), off.max()
     assert np.abs(gl.reshape(B, new, G) - lse).max() <= n / 32 * 2.0 ** -24 + 2.0 ** -22 * 17.5 + 2.0 ** -19
+
+
+CAPS = [1e-40, 0.5, 30.0, 1e4, 1e6, 1e8, 1e20, 1e38, 3.4028234e38]
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f16", 64), ("f32", 64)])
+@pytest.mark.parametrize("new", [1, 4, 8, 150])
+@pytest.mark.parametrize("cap", CAPS)
+def test_caps_of_any_size(dtype, d, new, cap):
+    """A cap's error counts by the capped score, which is at most the cap and at most the score."""
+    c = Case([500, 160], [new, min(new, 160)], H=2, G=4, d=d, P=32, dtype=dtype, seed=7, qscale=2.0)
+    page, row = c.at(0, np.arange(0, 500, 9))
+    c.K[page, :, row] = 0.0                                   # scores of 0
+    cap = float(np.float32(cap))
+    want = c.want(softcap=cap)
+    check(c, call(c, softcap=cap), want, np.minimum(cap, want[2]["zmax"])[:int(c.cu[-1])])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("new", [4, 8, 128])
+def test_a_rows_cap_does_not_depend_on_its_neighbours(dtype, new):
+    """Every other row's scores reach the cap, its neighbours' stay far below it."""
+    c = Case([400], [new], H=1, G=4, d=64, P=32, dtype=dtype, seed=11)
+    c.Q[1::2] *= 2.0 ** 17
+    want = c.want(softcap=2e5)
+    check(c, call(c, softcap=2e5), want, np.minimum(2e5, want[2]["zmax"]))
