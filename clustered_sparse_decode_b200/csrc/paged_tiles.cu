@@ -699,6 +699,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
         }
       }
       uint32_t again = __ballot_sync(kFull, valid && !fine);
+      __syncwarp();                    // what the rows' own threads have written is there before another overwrites it
       while (again) {
         const int src = __ffs(again) - 1;
         again &= again - 1;
