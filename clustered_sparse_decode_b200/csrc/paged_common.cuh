@@ -1,6 +1,6 @@
 // Definitions shared by the paged-cache operators: the arguments of an
-// attention call, a row's visible keys, and the exact row kernel body that the
-// fast kernels fall back on.
+// attention call, a row's visible keys, and what the kernels do about a row into
+// which a key that it does not see may have got.
 #pragma once
 
 #include <cuda.h>
@@ -97,48 +97,109 @@ __device__ __forceinline__ float score2(const Attend& a, float dot, float slope,
   return (z - slope * (float)abs(away)) * kLog2e;
 }
 
-// One row of one query head over the keys [k0, k1) that it sees, by one warp,
-// one key at a time, so that a key it does not see is not even read.  The
-// running maximum m is in base-2 units; lane l holds the elements
-// [l * D/32, (l + 1) * D/32) of the numerator.
+// A key that a row does not see has weight 0, but 0 times an infinite or NaN
+// value is NaN: only so, and only through a product that takes whole tiles of
+// keys, can it reach the row's numerator (its score is replaced, so never the
+// sum).  A row with a finite sum and a numerator that is not finite is therefore
+// looked at again.  Only a NaN that it sees itself explains the result: then it
+// stands, so that one NaN among a request's keys does not cost all later tokens a
+// second pass.  Otherwise (a NaN that it does not see; infinities, which rounded
+// weights and remainders can turn into NaN; no such value at all, where large
+// values have overflowed beside weights of up to 2^8) row_sum sums over the keys
+// that the row sees, with weights that add up to 1.
+enum { V_NAN = 1, V_INF = 2 };
+// whether such a row has to be summed again: `any` of all keys that went in, `unseen` of those that it does not see
+__device__ __forceinline__ bool sum_again(int any, bool inf, int unseen) {
+  return any != V_NAN || inf || unseen != 0;
+}
+
+// Which of V_NAN and V_INF the keys of [k0, k1) outside [lo, hi) hold.
+// [low, high): what the tile's rows see together; keys beyond it stand on the
+// page of the nearest one inside, as where a kernel loads them.  A warp together,
+// 4 KB in flight; `turns`, if given, counts up meanwhile.
 template <typename T, int D>
-struct RowState {
-  float m, l, acc[D / 32];
-};
+__device__ __noinline__ int odd_values(const Attend& a, int b, int h, int lo, int hi, int k0, int k1, int low, int high,
+                                       int* turns) {
+  constexpr int VEC = D * (int)sizeof(T) / 16, KEYS = 32 / VEC, U = 8;
+  const int lane = threadIdx.x & 31, mask = (1 << a.page_shift) - 1;
+  int odd = 0;
+#pragma unroll 1
+  for (int side = 0; side < 2; ++side) {
+    const int from = side ? max(hi, k0) : k0, to = side ? k1 : min(lo, k1);
+#pragma unroll 1
+    for (int j0 = from; j0 < to; j0 += KEYS * U) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int j = j0 + u * KEYS + lane / VEC;
+        if (j >= to) continue;
+        const int page = page_of(a, b, min(max(j, low), high - 1));
+        if (page < 0) continue;
+        const uint4 x = *reinterpret_cast<const uint4*>(a.V + page * a.page_b + h * a.head_b + (j & mask) * a.tok_b +
+                                                        lane % VEC * 16);
+        const T* e = reinterpret_cast<const T*>(&x);
+#pragma unroll
+        for (int i = 0; i < 16 / (int)sizeof(T); ++i) {
+          const float f = to_f32(e[i]);
+          odd |= f != f ? V_NAN : isfinite(f) ? 0 : V_INF;
+        }
+      }
+      if (turns && lane == 0) atomicAdd(turns, 1);
+      if (__any_sync(kFull, odd & V_INF)) return V_INF;
+    }
+  }
+  return __reduce_or_sync(kFull, odd);
+}
+
+// The sum 2^(z - m) v of one row of one query head over the keys of [k0, k1) that
+// it sees, by one warp; no other key is read.  Lane l gets the elements
+// [l * D/32, (l + 1) * D/32).  From the last key backwards, until nothing but NaN
+// is left: values that went bad at some token mostly stay so behind it.
 template <typename T, int D>
-__device__ void attend_row(const Attend& a, int b, const Request& r, int i, int hq, int k0, int k1, RowState<T, D>& s) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31, h = hq / a.G;
+__device__ __noinline__ void row_sum(const Attend& a, int b, const Request& r, int i, int hq, int k0, int k1, float m,
+                                       float (&acc)[D / 32], int* turns) {
+  constexpr int E = D / 32, U = 8;
+  const int lane = threadIdx.x & 31, h = hq / a.G, mask = (1 << a.page_shift) - 1;
   const Interval v = interval_of(a, r, prefix_of(a, b), i);
   const T* q = reinterpret_cast<const T*>(a.Q + (int64_t)(r.row0 + i) * a.q_row_b + (int64_t)hq * a.q_head_b) + lane * E;
   float qf[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) qf[e] = to_f32(q[e]);
   const float slope = a.slopes ? __ldg(a.slopes + hq) : 0.f;
-  s.m = -INFINITY;
-  s.l = 0.f;
 #pragma unroll
-  for (int e = 0; e < E; ++e) s.acc[e] = 0.f;
-  for (int j = max(k0, v.lo); j < min(k1, v.hi); ++j) {
-    const int page = page_of(a, b, j);
-    if (page < 0) continue;
-    const int64_t off = page * a.page_b + h * a.head_b + (j & ((1 << a.page_shift) - 1)) * a.tok_b;
-    const T* kr = reinterpret_cast<const T*>(a.K + off) + lane * E;
-    const T* vr = reinterpret_cast<const T*>(a.V + off) + lane * E;
-    float dot = 0.f;
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  const int from = max(k0, v.lo), to = min(k1, v.hi);
+#pragma unroll 1
+  for (int j0 = to - 1; j0 >= from; j0 -= U) {
+    float dot[U], val[U][E];
+    bool held[U];
 #pragma unroll
-    for (int e = 0; e < E; ++e) dot = fmaf(qf[e], to_f32(kr[e]), dot);
+    for (int u = 0; u < U; ++u) {
+      const int j = j0 - u, page = j >= from ? page_of(a, b, j) : -1;
+      held[u] = page >= 0;
+      const int64_t off = (held[u] ? page : 0) * a.page_b + h * a.head_b + (held[u] ? j & mask : 0) * a.tok_b;
+      dot[u] = 0.f;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(kFull, dot, o);
-    const float z = score2(a, dot, slope, v.pos - j);
-    const float m = fmaxf(s.m, z), keep = s.m == -INFINITY ? 0.f : exp2f(s.m - m);
-    const float w = z == -INFINITY ? 0.f : exp2f(z - m);
-    s.l = s.l * keep + w;
+      for (int e = 0; e < E; ++e) {
+        if (held[u]) dot[u] = fmaf(qf[e], to_f32(reinterpret_cast<const T*>(a.K + off)[lane * E + e]), dot[u]);
+        val[u][e] = held[u] ? to_f32(reinterpret_cast<const T*>(a.V + off)[lane * E + e]) : 0.f;
+      }
+    }
 #pragma unroll
-    for (int e = 0; e < E; ++e) s.acc[e] = s.acc[e] * keep + w * to_f32(vr[e]);
-    s.m = m;
+    for (int o = 16; o; o >>= 1)
+#pragma unroll
+      for (int u = 0; u < U; ++u) dot[u] += __shfl_xor_sync(kFull, dot[u], o);
+    bool gone = true;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float w = held[u] ? exp2f(score2(a, dot[u], slope, v.pos - (j0 - u)) - m) : 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(w, val[u][e], acc[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) gone = gone && acc[e] != acc[e];
+    if (turns && lane == 0) atomicAdd(turns, 1);
+    if (__all_sync(kFull, gone)) return;
   }
-  if (s.l != s.l) s.m = s.l;         // a NaN among the keys seen must not pass for "nothing seen"
 }
 
 }  // namespace paged

@@ -127,6 +127,8 @@ __global__ void __launch_bounds__(kF32Warps * 32) f32_kernel(const F32 f) {
     top = __reduce_max_sync(kFull, top);
     st.key0 = k0 + blk0 * kFewBlock;
     st.key1 = min(k0 + blk1 * kFewBlock, top);
+    st.low = low;
+    st.high = top;
     for (int c = tid; c < ROWS * D / 4; c += kF32Warps * 32) {
       const int row = c / (D / 4), d = c % (D / 4);
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -293,6 +295,56 @@ struct ManyCfg {
   static constexpr int SMEM = OFF_ROW + kManyRows * 16;
   static_assert(2 * SMEM <= 225 * 1024, "two blocks an SM");
 };
+
+// A warp's row of a unit: its result, or its state for the joining.  Lane l holds
+// the elements [l * D/32, (l + 1) * D/32).
+template <int D>
+struct ManyPut {
+  int row0, h;                         // the unit's first row of Q, KV head
+  float* slot;                         // of a partial result; null: the unit is whole
+  __device__ __forceinline__ void operator()(const Attend& a, int row, float top, float sum, const float* v) const {
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31, hq = h * a.G + row % a.G;
+    const int64_t t = row0 + row / a.G;
+    const bool none = sum == 0.f;
+    if (!slot) {
+      float* o = reinterpret_cast<float*>(a.O + t * a.o_row_b + (int64_t)hq * a.o_head_b) + lane * E;
+#pragma unroll
+      for (int c = 0; c < E; ++c) o[c] = none ? 0.f : v[c] / sum;
+      if (a.lse && lane == 0) a.lse[t * a.H * a.G + hq] = none ? -INFINITY : (top + log2f(sum)) / kLog2e;
+    } else {
+#pragma unroll
+      for (int c = 0; c < E; ++c) slot[2 * kManyRows + row * D + lane * E + c] = v[c];
+      if (lane == 0) {
+        slot[row] = none ? -INFINITY : top;
+        slot[kManyRows + row] = sum;
+      }
+    }
+  }
+};
+
+// Rows with a finite sum and a numerator that is not (sum_again): `again` and `inf`
+// of this warp's rows, `base` their maxima plus the logarithms of their sums.
+template <int D>
+__device__ __noinline__ void many_again(const Attend& a, int b, const Request r, int i0, int h, int cells, int key0, int key1,
+                                        int low, int high, uint32_t again, uint32_t inf, const float* base,
+                                        const ManyPut<D> put) {
+  const int warp = threadIdx.x >> 5, prefix = prefix_of(a, b);
+  const int end = min(key1, r.len), share = ((end - key0 + kManyWarps - 1) / kManyWarps + 15) & ~15, k0 = key0 + warp * share,
+            k1 = min(k0 + share, end);
+  const int odd = odd_values<float, D>(a, b, h, k1, k1, k0, k1, low, high, nullptr);
+  const int any = (__syncthreads_or(odd & V_NAN) ? V_NAN : 0) | (__syncthreads_or(odd & V_INF) ? V_INF : 0);
+  for (; again; again &= again - 1) {
+    const int k = __ffs(again) - 1, row = warp * kManyHeld + k, i = i0 + row / a.G;
+    if (row >= cells) continue;
+    const Interval v = interval_of(a, r, prefix, i);
+    const int unseen = any == V_NAN ? odd_values<float, D>(a, b, h, v.lo, v.hi, key0, end, low, high, nullptr) : 0;
+    if (!sum_again(any, inf >> k & 1u, unseen)) continue;
+    float sum[D / 32];
+    row_sum<float, D>(a, b, r, i, h * a.G + row % a.G, key0, end, base[k], sum, nullptr);
+    put(a, row, base[k], 1.f, sum);
+  }
+}
 
 template <int D>
 __global__ void __launch_bounds__(kManyWarps * 32, 2) f32_many_kernel(const F32 f) {
@@ -465,47 +517,35 @@ __global__ void __launch_bounds__(kManyWarps * 32, 2) f32_many_kernel(const F32 
       }
       __syncthreads();                 // the stage is read
     }
-    const bool whole = x == u0 && end == u1;
-    float* slot = f.w.part + (2 * (int64_t)part + (x == start ? 0 : 1)) * (int64_t)kManyRows * (2 + D);
-    auto put = [&](int row, float top, float sum, const float* v) {
-      const int i = i0 + row / a.G, hq = h * a.G + row % a.G;
-      const bool none = sum == 0.f;
-      if (whole) {
-        float* o = reinterpret_cast<float*>(a.O + (int64_t)(r.row0 + i) * a.o_row_b + (int64_t)hq * a.o_head_b) + lane * E;
-#pragma unroll
-        for (int c = 0; c < E; ++c) o[c] = none ? 0.f : v[c] / sum;
-        if (a.lse && lane == 0)
-          a.lse[(int64_t)(r.row0 + i) * a.H * a.G + hq] = none ? -INFINITY : (top + log2f(sum)) / kLog2e;
-      } else {
-#pragma unroll
-        for (int c = 0; c < E; ++c) slot[2 * kManyRows + row * D + lane * E + c] = v[c];
-        if (lane == 0) {
-          slot[row] = none ? -INFINITY : top;
-          slot[kManyRows + row] = sum;
-        }
-      }
-    };
-    uint32_t again = 0;
+    ManyPut<D> put{r.row0 + i0, h, nullptr};
+    if (x != u0 || end != u1) put.slot = f.w.part + (2 * (int64_t)part + (x == start ? 0 : 1)) * (int64_t)kManyRows * (2 + D);
+    uint32_t again = 0;                // rows to look at again
 #pragma unroll
     for (int k = 0; k < RW; ++k) {
       float sum = l[k];
 #pragma unroll
       for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-      bool fine = isfinite(sum);
+      bool fine = true;
 #pragma unroll
       for (int c = 0; c < E; ++c) fine = fine && isfinite(acc[k][c]);
+      fine = fine || !isfinite(sum) || sum == 0.f;
       again |= __all_sync(kFull, fine) ? 0u : 1u << k;
-      if (warp * RW + k < cells) put(warp * RW + k, m[k], sum, acc[k]);
+      if (warp * RW + k < cells) put(a, warp * RW + k, m[k], sum, acc[k]);
+      l[k] = sum;
     }
-    // a key that a row does not see may have been infinite or NaN: such rows key by key
-#pragma unroll 1
-    for (int k = 0; k < RW; ++k)
-      if ((again >> k & 1u) && warp * RW + k < cells) {
-        const int row = warp * RW + k;
-        RowState<float, D> s;
-        attend_row<float, D>(a, en.b, r, i0 + row / a.G, h * a.G + row % a.G, key0, key0 + tiles * kManyTile, s);
-        put(row, s.m, s.l, s.acc);
+    if (__syncthreads_or(again != 0)) {
+      uint32_t inf = 0;                // those of them with infinite numerators
+#pragma unroll
+      for (int k = 0; k < RW; ++k) {
+        bool large = false;
+#pragma unroll
+        for (int c = 0; c < E; ++c) large = large || isinf(acc[k][c]);
+        inf |= __any_sync(kFull, large) ? 1u << k : 0u;
+        if (lane == 0) pw[k] = m[k] + log2f(l[k]);
       }
+      __syncwarp();
+      many_again<D>(a, en.b, r, i0, h, cells, key0, key0 + tiles * kManyTile, low, top, again, inf, pw, put);
+    }
     __syncthreads();
     x = end;
   }

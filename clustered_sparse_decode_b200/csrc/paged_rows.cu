@@ -448,6 +448,8 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) few_kernel(const __grid_con
     st.cells = min(cells, ROWS);
     st.key0 = key0;
     st.key1 = key1;
+    st.low = lo_min;
+    st.high = hi_max;
     st.cluster = f.cluster;
     st.part = part;
     st.whole = !f.cluster && x == u0 && min(x1, u1) == u1;

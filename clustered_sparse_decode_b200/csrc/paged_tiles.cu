@@ -67,7 +67,7 @@ struct TilesCfg {
   static constexpr int OFF_KV = 2 * QB * STAGE;                       // [NS][KT][128 rows][128 B]
   static constexpr int OFF_BAR = OFF_KV + NS * STAGE;
   static constexpr int BARS = 2 * NS + 9 + 2 * QB + 2 * kItems;
-  static constexpr int OFF_ITEM = (OFF_BAR + BARS * 8 + 4 + 15) / 16 * 16;   // [kItems][16] words
+  static constexpr int OFF_ITEM = (OFF_BAR + BARS * 8 + 8 + 15) / 16 * 16;   // [kItems][16] words
   static constexpr int USED = OFF_ITEM + kItems * 64;
   static constexpr int SMEM = USED + 1024;
   static_assert(SMEM <= 232448, "shared memory of a block");
@@ -192,6 +192,32 @@ __device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+// Waits last two seconds at most, and longer only while rows are summed again
+// (`turns` counts up then), which takes as long as they have keys.
+__device__ __forceinline__ bool stuck(const int* turns, int& seen, int32_t* err) {
+  const int now = *reinterpret_cast<const volatile int*>(turns);
+  const bool same = now == seen;
+  seen = now;
+  if (same) set_error(err, E_TIMEOUT);
+  return same;
+}
+__device__ __forceinline__ bool poll_long(uint32_t bar, uint32_t parity, const int* turns, int32_t* err) {
+  long long end = sc::gtimer() + 2000000000LL;
+  int seen = *reinterpret_cast<const volatile int*>(turns);
+  for (uint32_t n = 1; !poll(bar, parity); ++n)
+    if ((n & 255u) == 0u && sc::gtimer() > end) {
+      if (stuck(turns, seen, err)) return false;
+      end = sc::gtimer() + 2000000000LL;
+    }
+  return true;
+}
+__device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity, const int* turns, int32_t* err) {
+  int seen = *reinterpret_cast<const volatile int*>(turns);
+  while (!sc::mbar_wait(bar, parity, sc::gtimer() + 2000000000LL))
+    if (stuck(turns, seen, err)) return false;
+  return true;
+}
+
 // ---------------------------------------------------------------------------
 // A block's items: the units, or parts of units, of its share
 // ---------------------------------------------------------------------------
@@ -210,11 +236,25 @@ struct Walk {
   int e;
 };
 
+// The keys [lo, hi) that the rows [i0, i1) of a request see together.  All lanes of a warp together.
+__device__ __forceinline__ void seen_by(const Attend& a, const Request& r, int prefix, int i0, int i1, int& lo, int& hi) {
+  lo = INT32_MAX;
+  hi = 0;
+  for (int i = i0 + (threadIdx.x & 31); i < i1; i += 32) {
+    const Interval v = interval_of(a, r, prefix, i);
+    if (v.hi > v.lo) {
+      lo = min(lo, v.lo);
+      hi = max(hi, v.hi);
+    }
+  }
+  lo = __reduce_min_sync(kFull, lo);
+  hi = __reduce_max_sync(kFull, hi);
+}
+
 // The next item, or false at the share's end.  All lanes of a warp together.
 __device__ __forceinline__ bool next_item(const Tiles& f, Walk& w, Item& it) {
   if (w.x >= w.x1) return false;
   const Attend& a = f.a;
-  const int lane = threadIdx.x & 31;
   while (f.w.before[w.e + 1] * a.H <= w.x) ++w.e;
   const int64_t first = f.w.before[w.e] * a.H, n = f.w.before[w.e + 1] - f.w.before[w.e];
   const Entry en = f.w.entry[w.e];
@@ -232,17 +272,9 @@ __device__ __forceinline__ bool next_item(const Tiles& f, Walk& w, Item& it) {
   it.hi = 0;
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
-    int lo = INT32_MAX, hi = 0;
-    const int i0 = it.i0 + g * (f.tile / 2), i1 = min(it.r.n, i0 + f.tile / 2);
-    for (int i = i0 + lane; i < i1; i += 32) {
-      const Interval v = interval_of(a, it.r, prefix, i);
-      if (v.hi > v.lo) {
-        lo = min(lo, v.lo);
-        hi = max(hi, v.hi);
-      }
-    }
-    lo = __reduce_min_sync(kFull, lo);
-    hi = __reduce_max_sync(kFull, hi);
+    const int i0 = it.i0 + g * (f.tile / 2);
+    int lo, hi;
+    seen_by(a, it.r, prefix, i0, min(it.r.n, i0 + f.tile / 2), lo, hi);
     it.lo = min(it.lo, lo);
     it.hi = max(it.hi, hi);
     it.from[g] = hi > lo ? max(0, min(it.nb, (lo - it.key0) >> 7)) : 0;
@@ -253,23 +285,54 @@ __device__ __forceinline__ bool next_item(const Tiles& f, Walk& w, Item& it) {
   return true;
 }
 
-// One row done again, out of line: it is rare and needs registers.
+// A warp's rows with a finite sum and a numerator that is not (sum_again), out of
+// line: they are rare and need registers.  `rows`: the lanes of such rows; tO, i, hq,
+// m, l: this lane's numerators and row; the keys [k0, k1) went into the products.
+// `slot`: of the partial result, at this warp's first row, or null.  A row that sees
+// no key is 0.
 template <typename T, int D>
-__device__ __noinline__ void row_again(const Attend* a, int b, const Request* r, int i, int hq, int k0, int k1, bool whole,
-                                       float* m, float* l, float* num) {
-  RowState<T, D> s;
-  attend_row<T, D>(*a, b, *r, i, hq, k0, k1, s);
-  const int lane = threadIdx.x & 31;
-  if (whole) {
-    T* o = reinterpret_cast<T*>(a->O + (int64_t)(r->row0 + i) * a->o_row_b + (int64_t)hq * a->o_head_b) + lane * (D / 32);
+__device__ __noinline__ void rows_again(const Attend& a, int b, const Request r, int tile0, int tile, uint32_t rows,
+                                        uint32_t tO, int i, int hq, float m, float l, int k0, int k1, float* slot,
+                                        float* num, int* turns) {
+  const int lane = threadIdx.x & 31, prefix = prefix_of(a, b), h = __shfl_sync(kFull, hq, __ffs(rows) - 1) / a.G;
+  int low, high;
+  seen_by(a, r, prefix, tile0, min(r.n, tile0 + tile), low, high);
+  k1 = min(k1, r.len);
+  const int any = odd_values<T, D>(a, b, h, k1, k1, k0, k1, low, high, turns);
+  bool large = false;
+#pragma unroll 1
+  for (int k = 0; k < D; k += 32) {
+    float o[32];
+    tmem_ld(tO + k, o);
+    tmem_ld_wait(o);
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) o[e] = from_f32<T>(s.l == 0.f ? 0.f : s.acc[e] / s.l);
-    if (a->lse && lane == 0)
-      a->lse[(int64_t)(r->row0 + i) * a->H * a->G + hq] = s.l == 0.f ? -INFINITY : (s.m + log2f(s.l)) / kLog2e;
-  } else {
-    if (lane == 0) { *m = s.m; *l = s.l; }
+    for (int q = 0; q < 32; ++q) large |= fabsf(o[q]) > 3.4028235e38f;
+  }
+  const uint32_t inf = __ballot_sync(kFull, large), none = __ballot_sync(kFull, l == 0.f);
+  for (; rows; rows &= rows - 1) {
+    const int src = __ffs(rows) - 1, ri = __shfl_sync(kFull, i, src), rh = __shfl_sync(kFull, hq, src);
+    const float base = __shfl_sync(kFull, m + log2f(l), src);
+    const Interval v = interval_of(a, r, prefix, ri);
+    float s[D / 32] = {};
+    if (none >> src & 1u) {
+      if (slot) continue;
+    } else {
+      const int unseen = any == V_NAN ? odd_values<T, D>(a, b, h, v.lo, v.hi, k0, k1, low, high, turns) : 0;
+      if (!sum_again(any, inf >> src & 1u, unseen)) continue;
+      row_sum<T, D>(a, b, r, ri, rh, k0, k1, base, s, turns);
+    }
+    if (slot) {
+      if (lane == 0) {
+        slot[src] = base;
+        slot[2 * kHalf + src] = 1.f;
+      }
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) num[lane * (D / 32) + e] = s.acc[e];
+      for (int e = 0; e < D / 32; ++e) num[src * D + lane * (D / 32) + e] = s[e];
+    } else {
+      T* o = reinterpret_cast<T*>(a.O + (int64_t)(r.row0 + ri) * a.o_row_b + (int64_t)rh * a.o_head_b) + lane * (D / 32);
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) o[e] = from_f32<T>(s[e]);
+    }
   }
 }
 
@@ -362,8 +425,10 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
                  s_full = q_empty + 8 * C::QB, p_full = s_full + 16, o_full = p_full + 32, drain = o_full + 16,
                  item_full = drain + 8, item_empty = item_full + 8 * kItems;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + C::BARS * 8);
+  int* turns = reinterpret_cast<int*>(tmem_slot + 1);    // counts up while rows are done again
 
   if (threadIdx.x == 0) {
+    *turns = 0;
     for (int s = 0; s < NS; ++s) {
       sc::mbar_init(kv_full + 8 * s, 1);
       sc::mbar_init(kv_empty + 8 * s, 1);
@@ -401,21 +466,11 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
   const int part = blockIdx.x;
   Item it;
   bool ok = true;
-  auto wait_one = [&](uint32_t bar, uint32_t parity) {   // this thread alone; two seconds at most
-    if (poll(bar, parity)) return true;
-    const long long end = sc::gtimer() + 2000000000LL;
-    for (uint32_t n = 1; !poll(bar, parity); ++n)
-      if ((n & 255u) == 0u && sc::gtimer() > end) {
-        set_error(a.err, E_TIMEOUT);
-        return false;
-      }
-    return true;
+  auto wait_one = [&](uint32_t bar, uint32_t parity) {   // this thread alone
+    return poll(bar, parity) || poll_long(bar, parity, turns, a.err);
   };
   auto wait = [&](uint32_t bar, uint32_t parity) {       // a warp together; after one failure at once
-    if (ok && !sc::mbar_try(bar, parity) && !sc::mbar_wait(bar, parity, sc::gtimer() + 2000000000LL)) {
-      set_error(a.err, E_TIMEOUT);
-      ok = false;
-    }
+    ok = ok && (sc::mbar_try(bar, parity) || wait_long(bar, parity, turns, a.err));
     return ok = __all_sync(kFull, ok);
   };
 
@@ -657,7 +712,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
         tc_after();
       }
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      bool fine = l == l;
+      bool finite = true;
 #pragma unroll 1
       for (int k = 0; k < D; k += 32) {
         float o[32];
@@ -670,7 +725,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
           tmem_ld_wait(o);
         }
 #pragma unroll
-        for (int q = 0; q < 32; ++q) fine &= fabsf(o[q]) <= 3.4028235e38f;
+        for (int q = 0; q < 32; ++q) finite &= fabsf(o[q]) <= 3.4028235e38f;
         if (!valid) continue;
         if (it.whole) {
 #pragma unroll
@@ -688,7 +743,6 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
             *reinterpret_cast<float4*>(num + k + q) = make_float4(o[q], o[q + 1], o[q + 2], o[q + 3]);
         }
       }
-      tc_before();
       if (valid) {
         if (it.whole) {
           if (a.lse)
@@ -698,16 +752,12 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
           slot[2 * kHalf + cell] = l;
         }
       }
-      uint32_t again = __ballot_sync(kFull, valid && !fine);
+      const uint32_t again = __ballot_sync(kFull, valid && !finite && l == l);       // (not where the sum is NaN)
       __syncwarp();                    // what the rows' own threads have written is there before another overwrites it
-      while (again) {
-        const int src = __ffs(again) - 1;
-        again &= again - 1;
-        const int ri = __shfl_sync(kFull, i, src), rh = __shfl_sync(kFull, hq, src), rc = __shfl_sync(kFull, cell, src);
-        const Request r = it.r;
-        row_again<T, D>(&a, it.b, &r, ri, rh, it.key0, it.key0 + it.nb * kKeys, it.whole, slot + rc,
-                        slot + 2 * kHalf + rc, slot + 2 * (2 * kHalf) + (int64_t)rc * D);
-      }
+      if (again)
+        rows_again<T, D>(a, it.b, it.r, it.i0, f.tile, again, tO, i, hq, m - kLift<T>, l, it.key0 + it.from[g] * kKeys,
+                         it.key0 + it.to[g] * kKeys, it.whole ? nullptr : slot + cell - lane, num - (int64_t)lane * D, turns);
+      tc_before();
       if (it.to[0] > it.from[0] || it.to[1] > it.from[1]) n_kv += 2 * it.nb;
     }
   } else {

@@ -103,35 +103,66 @@ __device__ __forceinline__ void span_of(const Attend& a, const Request& r, int b
 // the scratch, or, in a cluster that shares the unit, the cluster's result.
 struct Settle {
   int b, h, i0, cells, key0, key1;     // request, KV head, first token, (token, head) rows, keys
+  int low, high;                       // keys that its rows see together
   Request r;
   int cluster, part;                   // blocks of the cluster (0: none), this block's place
   bool whole;                          // the unit is this block's alone
   float* slot;                         // of a partial result
 };
+template <typename T>
+__device__ __forceinline__ void settle_final(const Attend& a, const Settle& s, int row, int c, float m, float l, float v) {
+  const bool none = l == 0.f;
+  const int64_t t = s.r.row0 + s.i0 + row / a.G, hq = s.h * a.G + row % a.G;
+  reinterpret_cast<T*>(a.O + t * a.o_row_b + hq * a.o_head_b)[c] = from_f32<T>(none ? 0.f : v / l);
+  if (a.lse && c == 0) a.lse[t * a.H * a.G + hq] = none ? -INFINITY : (m + log2f(l)) / kLog2e;
+}
+template <typename T, int D, int ROWS, int PITCH>
+__device__ __forceinline__ void settle_put(const Attend& a, const Settle& s, float* num, float* unit, int row, int c, float m,
+                                           float l, float v) {
+  if (s.cluster) {                     // warp 0's numerators are replaced, each by the thread that read it
+    num[row * PITCH + c] = v;
+    if (c == 0) { unit[row] = m; unit[ROWS + row] = l; }
+  } else if (s.whole) {
+    settle_final<T>(a, s, row, c, m, l, v);
+  } else {
+    s.slot[2 * ROWS + row * D + c] = v;
+    if (c == 0) { s.slot[row] = m; s.slot[ROWS + row] = l; }
+  }
+}
+// Rows with a finite sum and a numerator that is not (sum_again): out of line, for the registers' sake.
+template <typename T, int D, int ROWS, int PITCH, int WARPS>
+__device__ __noinline__ void settle_again(const Attend& a, const Settle s, const float* ml, float* num, float* unit,
+                                          const int* bad) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int end = min((s.key1 + 15) & ~15, s.r.len);         // of the 16-key tiles
+  const int part = ((end - s.key0 + WARPS - 1) / WARPS + 15) & ~15, k0 = s.key0 + warp * part, k1 = min(k0 + part, end);
+  const int odd = odd_values<T, D>(a, s.b, s.h, k1, k1, k0, k1, s.low, s.high, nullptr);
+  const int any = (__syncthreads_or(odd & V_NAN) ? V_NAN : 0) | (__syncthreads_or(odd & V_INF) ? V_INF : 0);
+  for (int row = warp; row < s.cells; row += WARPS) {
+    if (!bad[row]) continue;
+    const int i = s.i0 + row / a.G;
+    const Interval x = interval_of(a, s.r, prefix_of(a, s.b), i);
+    const int unseen = any == V_NAN ? odd_values<T, D>(a, s.b, s.h, x.lo, x.hi, s.key0, end, s.low, s.high, nullptr) : 0;
+    if (!sum_again(any, bad[row] & V_INF, unseen)) continue;
+    float m = -INFINITY, l = 0.f, v[D / 32];
+    for (int w = 0; w < WARPS; ++w) m = fmaxf(m, ml[(w * 2) * ROWS + row]);
+    for (int w = 0; w < WARPS; ++w) {
+      const float mw = ml[(w * 2) * ROWS + row];
+      l = fmaf(mw == -INFINITY ? 0.f : exp2f(mw - m), ml[(w * 2 + 1) * ROWS + row], l);
+    }
+    m += log2f(l);
+    row_sum<T, D>(a, s.b, s.r, i, s.h * a.G + row % a.G, s.key0, s.key1, m, v, nullptr);
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) settle_put<T, D, ROWS, PITCH>(a, s, num, unit, row, lane * (D / 32) + e, m, 1.f, v[e]);
+  }
+}
 template <typename T, int D, int ROWS, int PITCH, int WARPS>
 __device__ void settle(const Attend& a, const Settle& s, const float* ml, float* num, int stride, float* unit, int* bad) {
   namespace cg = cooperative_groups;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t Hq = (int64_t)a.H * a.G;
-  auto final = [&](int row, int c, float m, float l, float v) {
-    const bool none = l == 0.f;
-    const int64_t t = s.r.row0 + s.i0 + row / a.G, hq = s.h * a.G + row % a.G;
-    reinterpret_cast<T*>(a.O + t * a.o_row_b + hq * a.o_head_b)[c] = from_f32<T>(none ? 0.f : v / l);
-    if (a.lse && c == 0) a.lse[t * Hq + hq] = none ? -INFINITY : (m + log2f(l)) / kLog2e;
-  };
-  auto put = [&](int row, int c, float m, float l, float v) {
-    if (s.cluster) {                   // warp 0's numerators are replaced, each by the thread that read it
-      num[row * PITCH + c] = v;
-      if (c == 0) { unit[row] = m; unit[ROWS + row] = l; }
-    } else if (s.whole) {
-      final(row, c, m, l, v);
-    } else {
-      s.slot[2 * ROWS + row * D + c] = v;
-      if (c == 0) { s.slot[row] = m; s.slot[ROWS + row] = l; }
-    }
-  };
+  const int tid = threadIdx.x;
   if (tid < ROWS) bad[tid] = 0;
   __syncthreads();
+  bool mine = false;
   for (int row = tid / D; row < s.cells; row += WARPS * 32 / D) {
     const int c = tid % D;
     float m = -INFINITY, l = 0.f, v = 0.f;
@@ -143,18 +174,13 @@ __device__ void settle(const Attend& a, const Settle& s, const float* ml, float*
       l = fmaf(k, ml[(w * 2 + 1) * ROWS + row], l);
       v = fmaf(k, num[w * stride + row * PITCH + c], v);
     }
-    // a key that the row does not see can reach its numerator as 0 * (infinity or NaN), and only so
-    if (!isfinite(v) || !isfinite(l)) bad[row] = 1;
-    put(row, c, m, l, v);
-  }
-  __syncthreads();
-  for (int row = warp; row < s.cells; row += WARPS)
-    if (bad[row]) {
-      RowState<T, D> x;
-      attend_row<T, D>(a, s.b, s.r, s.i0 + row / a.G, s.h * a.G + row % a.G, s.key0, s.key1, x);
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) put(row, lane * (D / 32) + i, x.m, x.l, x.acc[i]);
+    if (!isfinite(v) && isfinite(l) && l > 0.f) {
+      atomicOr(bad + row, v != v ? V_NAN : V_INF);
+      mine = true;
     }
+    settle_put<T, D, ROWS, PITCH>(a, s, num, unit, row, c, m, l, v);
+  }
+  if (__syncthreads_or(mine)) settle_again<T, D, ROWS, PITCH, WARPS>(a, s, ml, num, unit, bad);
   if (!s.cluster) return;
   cg::cluster_group cl = cg::this_cluster();
   cl.sync();
@@ -167,7 +193,7 @@ __device__ void settle(const Attend& a, const Settle& s, const float* ml, float*
       l = fmaf(k, cl.map_shared_rank(unit, p)[ROWS + row], l);
       if (k != 0.f) v = fmaf(k, cl.map_shared_rank(num, p)[row * PITCH + c], v);
     }
-    final(row, c, m, l, v);
+    settle_final<T>(a, s, row, c, m, l, v);
   }
   cl.sync();                           // no block leaves while its state is read
 }

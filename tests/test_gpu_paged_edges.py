@@ -1,8 +1,9 @@
 """Paged-cache calls at the edges of what their documentation allows."""
 import numpy as np
 import pytest
+import torch
 
-from paged_cases import Case, bounds, cache_of, call
+from paged_cases import TDT, Case, bounds, cache_of, call
 
 pytestmark = pytest.mark.gpu
 
@@ -21,3 +22,44 @@ def test_rows_done_again_are_the_ones_that_stay(dtype, d, n, new):
     for _ in range(10):
         got = call(c, cache=cache, first_key=first)
         assert (np.abs(got[0] - want[0]) <= tol).all()
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f16", 64), ("f32", 64)])
+@pytest.mark.parametrize("new", [1, 6, 300])
+@pytest.mark.parametrize("kind", ["one_value", "all_behind"])
+def test_bad_values_of_one_request_stay_its_own(dtype, d, new, kind):
+    """An early NaN and a late infinity among one long request's values: in its own rows where they belong, in the
+    columns that hold them, and nowhere else; other requests' rows are written as without it."""
+    c = Case([16400, 16400, 700], [new] * 3, H=1, G=4, d=d, P=64, dtype=dtype, seed=31)
+    want = c.want()
+    tol, ltol = bounds(c, want[2], want[0], want[1])
+    late = 16400 - min(50, new // 2 + 1)
+    for j, col, bad in ((5, 3, np.nan), (late, 7, np.inf)):
+        j = np.arange(j, 16400 if kind == "all_behind" and bad == np.inf else j + 1)
+        page, row = c.at(0, j)
+        c.V[page, 0, row, col] = bad
+    O = want[0].copy()
+    pos = np.arange(16400 - new, 16400)
+    O[:new, :, 3] = np.nan
+    O[np.arange(new)[pos >= late], :, 7] = np.inf
+    got = call(c)
+    odd = ~np.isfinite(O)
+    assert np.array_equal(got[0][odd], O[odd], equal_nan=True)
+    assert (np.abs(got[0][~odd] - O[~odd]) <= tol[~odd]).all()
+    assert (np.abs(got[1] - want[1]) <= ltol).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("new", [1, 6, 100])
+def test_values_near_the_types_largest(dtype, new):
+    """Weights of up to 2^8 times the largest finite value pass fp32's range; the average of the values does not."""
+    c = Case([900], [new], H=1, G=4, d=64, P=32, dtype=dtype, seed=13)
+    top = torch.finfo(TDT[dtype]).max
+    for j, col in ((3, 1), (500, 5), (700, 9), (810, 60)):
+        page, row = c.at(0, j)
+        c.V[page, 0, row, col] = top if j % 2 else -top
+    want = c.want()
+    got = call(c)
+    tol = bounds(c, want[2], want[0], want[1])[0]
+    assert np.isfinite(got[0]).all()
+    assert (np.abs(got[0] - want[0]) <= tol).all()
