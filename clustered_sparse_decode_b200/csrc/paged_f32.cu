@@ -44,7 +44,7 @@ struct F32Cfg {
   static constexpr int OFF_ML = OFF_Q + ROWS * D * 4;
   static constexpr int OFF_UNIT = OFF_ML + kF32Warps * 2 * ROWS * 4;
   static constexpr int OFF_BAD = OFF_UNIT + 2 * ROWS * 4;
-  static constexpr int SMEM = OFF_BAD + ROWS * 4;
+  static constexpr int SMEM = OFF_BAD + (int)sizeof(Again<ROWS>);
   static_assert(ROWS * PITCH * 4 <= NS * STAGE, "a warp's numerators fit its ring");
   static_assert(SMEM <= 227 * 1024 && WARP % 16 == 0 && STAGE % 16 == 0, "shared memory");
 };
@@ -60,6 +60,7 @@ __global__ void __launch_bounds__(kF32Warps * 32) f32_kernel(const F32 f) {
   float* pw = reinterpret_cast<float*>(smem + warp * C::WARP + NS * C::STAGE);     // [16 keys][ROWS]
   float* q = reinterpret_cast<float*>(smem + C::OFF_Q);
   float* ml = reinterpret_cast<float*>(smem + C::OFF_ML);
+  Again<ROWS>* again = reinterpret_cast<Again<ROWS>*>(smem + C::OFF_BAD);
   const uint32_t ring_s = sc::smem_u32(ring);
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
@@ -127,8 +128,10 @@ __global__ void __launch_bounds__(kF32Warps * 32) f32_kernel(const F32 f) {
     top = __reduce_max_sync(kFull, top);
     st.key0 = k0 + blk0 * kFewBlock;
     st.key1 = min(k0 + blk1 * kFewBlock, top);
-    st.low = low;
-    st.high = top;
+    if (tid == 0) {
+      again->low = low;
+      again->high = top;
+    }
     for (int c = tid; c < ROWS * D / 4; c += kF32Warps * 32) {
       const int row = c / (D / 4), d = c % (D / 4);
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -262,7 +265,7 @@ __global__ void __launch_bounds__(kF32Warps * 32) f32_kernel(const F32 f) {
     st.slot = f.cluster ? nullptr : f.w.part + (2 * (int64_t)part + (x == start ? 0 : 1)) * (int64_t)ROWS * (2 + D);
     settle<float, D, ROWS, C::PITCH, kF32Warps>(a, st, ml, reinterpret_cast<float*>(smem), C::WARP / 4,
                                                 reinterpret_cast<float*>(smem + C::OFF_UNIT),
-                                                reinterpret_cast<int*>(smem + C::OFF_BAD));
+                                                again);
     if (f.cluster) return;
     __syncthreads();
     x = min(x1, u1);
@@ -323,26 +326,50 @@ struct ManyPut {
   }
 };
 
-// Rows with a finite sum and a numerator that is not (sum_again): `again` and `inf`
-// of this warp's rows, `base` their maxima plus the logarithms of their sums.
+// Rows with a finite sum and a numerator that is not (mend_rows), `again` of this
+// warp's: ml holds their maxima and sums, num their numerators.
 template <int D>
 __device__ __noinline__ void many_again(const Attend& a, int b, const Request r, int i0, int h, int cells, int key0, int key1,
-                                        int low, int high, uint32_t again, uint32_t inf, const float* base,
+                                        int low, int high, uint32_t again, const float* ml, const float* num,
                                         const ManyPut<D> put) {
-  const int warp = threadIdx.x >> 5, prefix = prefix_of(a, b);
-  const int end = min(key1, r.len), share = ((end - key0 + kManyWarps - 1) / kManyWarps + 15) & ~15, k0 = key0 + warp * share,
-            k1 = min(k0 + share, end);
-  const int odd = odd_values<float, D>(a, b, h, k1, k1, k0, k1, low, high, nullptr);
-  const int any = (__syncthreads_or(odd & V_NAN) ? V_NAN : 0) | (__syncthreads_or(odd & V_INF) ? V_INF : 0);
-  for (; again; again &= again - 1) {
-    const int k = __ffs(again) - 1, row = warp * kManyHeld + k, i = i0 + row / a.G;
-    if (row >= cells) continue;
-    const Interval v = interval_of(a, r, prefix, i);
-    const int unseen = any == V_NAN ? odd_values<float, D>(a, b, h, v.lo, v.hi, key0, end, low, high, nullptr) : 0;
-    if (!sum_again(any, inf >> k & 1u, unseen)) continue;
-    float sum[D / 32];
-    row_sum<float, D>(a, b, r, i, h * a.G + row % a.G, key0, end, base[k], sum, nullptr);
-    put(a, row, base[k], 1.f, sum);
+  constexpr int E = D / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, prefix = prefix_of(a, b);
+  const int rows = min(kManyHeld, cells - warp * kManyHeld);
+  again &= rows > 0 ? (1u << rows) - 1 : 0u;
+  if (again == 0) return;
+  int c0 = key0, c1 = min(key1, r.len), common[E] = {};     // the keys that all of them see
+  for (uint32_t x = again; x; x &= x - 1) {
+    const Interval v = interval_of(a, r, prefix, i0 + (warp * kManyHeld + __ffs(x) - 1) / a.G);
+    c0 = max(c0, v.lo);
+    c1 = min(c1, v.hi);
+  }
+  c1 = max(c0, c1);
+  odd_values<float, D>(a, b, h, c0, c1, low, high, common, nullptr);
+  while (again) {
+    Rows4 rows;
+    int at[4];
+    float v[4][E] = {};
+    rows.n = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (!again) continue;
+      at[k] = __ffs(again) - 1;
+      again &= again - 1;
+      const int row = warp * kManyHeld + at[k];
+      rows.i[k] = i0 + row / a.G;
+      rows.hq[k] = h * a.G + row % a.G;
+      rows.base[k] = ml[at[k]] + log2f(ml[kManyHeld + at[k]]);
+      rows.n = k + 1;
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[k][e] = num[at[k] * D + lane * E + e];
+    }
+    const uint32_t done = mend_rows<float, D>(a, b, r, rows, key0, key1, low, high, c0, c1, common, v, nullptr);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k >= rows.n) continue;
+      const bool one = done >> k & 1u;
+      put(a, warp * kManyHeld + at[k], one ? rows.base[k] : ml[at[k]], one ? 1.f : ml[kManyHeld + at[k]], v[k]);
+    }
   }
 }
 
@@ -533,18 +560,18 @@ __global__ void __launch_bounds__(kManyWarps * 32, 2) f32_many_kernel(const F32 
       if (warp * RW + k < cells) put(a, warp * RW + k, m[k], sum, acc[k]);
       l[k] = sum;
     }
-    if (__syncthreads_or(again != 0)) {
-      uint32_t inf = 0;                // those of them with infinite numerators
+    if (again) {                       // (the queries and weights in shared memory are this warp's own)
 #pragma unroll
       for (int k = 0; k < RW; ++k) {
-        bool large = false;
 #pragma unroll
-        for (int c = 0; c < E; ++c) large = large || isinf(acc[k][c]);
-        inf |= __any_sync(kFull, large) ? 1u << k : 0u;
-        if (lane == 0) pw[k] = m[k] + log2f(l[k]);
+        for (int c = 0; c < E; ++c) q[k * D + lane * E + c] = acc[k][c];
+        if (lane == 0) {
+          pw[k] = m[k];
+          pw[RW + k] = l[k];
+        }
       }
       __syncwarp();
-      many_again<D>(a, en.b, r, i0, h, cells, key0, key0 + tiles * kManyTile, low, top, again, inf, pw, put);
+      many_again<D>(a, en.b, r, i0, h, cells, key0, key0 + tiles * kManyTile, low, top, again, pw, q, put);
     }
     __syncthreads();
     x = end;

@@ -91,11 +91,12 @@ struct FewCfg {
   static constexpr int OFF_BAR = kFewWarps * kRing;                   // [warps][NS] barriers
   static constexpr int OFF_ML = OFF_BAR + kFewWarps * NS * 8;         // [warps][2][ROWS] maxima, sums
   static constexpr int OFF_UNIT = OFF_ML + kFewWarps * 2 * ROWS * 4;  // [2][ROWS] maxima, sums of the block
-  static constexpr int OFF_BAD = OFF_UNIT + 2 * ROWS * 4;             // [ROWS] rows to be done again
-  static constexpr int OFF_LIST = (OFF_BAD + ROWS * 4 + 7) / 8 * 8;   // [kOwnList + 1] blocks before each request
+  static constexpr int OFF_BAD = OFF_UNIT + 2 * ROWS * 4;             // rows to be looked at again
+  static constexpr int OFF_LIST = (OFF_BAD + (int)sizeof(Again<ROWS>) + 7) / 8 * 8;   // [kOwnList + 1] blocks before each request
   static constexpr int OFF_KEY = OFF_LIST + (kOwnList + 1) * 8;       // [kOwnList] first keys
   static constexpr int OFF_SUM = OFF_KEY + kOwnList * 4;              // [warps] sums
-  static constexpr int USED = OFF_SUM + kFewWarps * 8;
+  static constexpr int OFF_ROW = (OFF_SUM + kFewWarps * 8 + 15) / 16 * 16;   // [warps][ROWS] first key, end, position, slope
+  static constexpr int USED = OFF_ROW + kFewWarps * ROWS * 16;
   static constexpr int SMEM = USED + 1024;                            // room to align
   static_assert(ROWS * PITCH * 4 <= kRing, "a warp's numerators fit its ring");
   static_assert(2 * SMEM <= 227 * 1024, "two blocks an SM");
@@ -114,7 +115,8 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) few_kernel(const __grid_con
   float* num = reinterpret_cast<float*>(smem + warp * kRing);         // this warp's numerators, at a share's end
   float* ml = reinterpret_cast<float*>(smem + C::OFF_ML);
   float* unit_m = reinterpret_cast<float*>(smem + C::OFF_UNIT);
-  int* bad = reinterpret_cast<int*>(smem + C::OFF_BAD);
+  Again<ROWS>* again = reinterpret_cast<Again<ROWS>*>(smem + C::OFF_BAD);
+  int4* mine = reinterpret_cast<int4*>(smem + C::OFF_ROW) + warp * ROWS;
 
   if (lane == 0)
     for (int s = 0; s < NS; ++s) sc::mbar_init(bars + 8 * s, 1);
@@ -211,25 +213,22 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) few_kernel(const __grid_con
     }
     const Request r = request_of(a, b);
     const int prefix = prefix_of(a, b), cells = r.n * a.G;
-    // this lane's rows (g and g + 8 of each tile) and what the rows see together
-    int lo[MT][2], hi[MT][2], pos[MT][2];
-    float slope[MT][2];
+    // this lane's rows (g and g + 8 of each tile) and what the rows see together; a row's own keys, position and slope
+    // are kept in shared memory (in registers they cost those that the two tiles of 17 to 32 rows lack)
     int lo_min = INT32_MAX, lo_max = 0, hi_min = INT32_MAX, hi_max = 0;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const int row = DUP ? g : mt * 16 + s * 8 + g;
-        lo[mt][s] = 0;
-        hi[mt][s] = INT32_MAX;
-        pos[mt][s] = 0;
-        slope[mt][s] = 0.f;
-        if (row >= cells) continue;
+        if (row >= cells) {
+          if (t4 == 0) mine[row] = make_int4(0, INT32_MAX, 0, 0);
+          continue;
+        }
         const Interval v = interval_of(a, r, prefix, row / a.G);
-        lo[mt][s] = v.lo;
-        hi[mt][s] = v.hi;
-        pos[mt][s] = v.pos;
-        if (a.slopes) slope[mt][s] = __ldg(a.slopes + h * a.G + row % a.G) * kLog2e;
+        if (t4 == 0)
+          mine[row] = make_int4(v.lo, v.hi, v.pos,
+                                a.slopes ? __float_as_int(__ldg(a.slopes + h * a.G + row % a.G) * kLog2e) : 0);
         lo_max = max(lo_max, v.lo);
         hi_min = min(hi_min, v.hi);
         if (v.hi > v.lo) {
@@ -237,6 +236,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) few_kernel(const __grid_con
           hi_max = max(hi_max, v.hi);
         }
       }
+    __syncwarp();
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) {
       lo_min = min(lo_min, __shfl_xor_sync(kFull, lo_min, o));
@@ -251,6 +251,10 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) few_kernel(const __grid_con
       blk1 = (int)((int64_t)n * (part + 1) / f.cluster);
     }
     const int key0 = k0 + blk0 * kFewBlock, key1 = min(k0 + blk1 * kFewBlock, hi_max);
+    if (tid == 0) {
+      again->low = lo_min;
+      again->high = hi_max;
+    }
 
     uint32_t qf[MT][KS][4];
 #pragma unroll
@@ -342,20 +346,33 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) few_kernel(const __grid_con
           }
         }
         const bool whole = j0 >= lo_max && j0 + kTile <= hi_min;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            float& v = z[mt][c >> 2][c & 3];
+            v = a.cap > 0.f ? cap_of(a, v) : v * a.to_z;
+          }
+        if (!whole || a.slopes) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int hrow = 0; hrow < 2; ++hrow) {
+              const int4 x = mine[DUP ? g : mt * 16 + hrow * 8 + g];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                float& v = z[mt][k >> 1][2 * hrow + (k & 1)];
+                const int j = j0 + (k >> 1) * 8 + 2 * t4 + (k & 1);
+                if (a.slopes) v -= __int_as_float(x.w) * (float)abs(x.z - j);
+                if (j < x.x || j >= x.y) v = -INFINITY;
+              }
+            }
+        }
         bool grow = false;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int nh = 0; nh < 2; ++nh)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              float v = a.cap > 0.f ? cap_of(a, z[mt][nh][c]) : z[mt][nh][c] * a.to_z;
-              const int j = j0 + nh * 8 + 2 * t4 + (c & 1), hrow = c >> 1;
-              if (a.slopes) v -= slope[mt][hrow] * (float)abs(pos[mt][hrow] - j);
-              if (!whole && (j < lo[mt][hrow] || j >= hi[mt][hrow])) v = -INFINITY;
-              z[mt][nh][c] = v;
-              grow |= v > m[mt][hrow] + kLazyLimit;
-            }
+          for (int c = 0; c < 8; ++c) grow |= z[mt][c >> 2][c & 3] > m[mt][(c & 3) >> 1] + kLazyLimit;
         if (__any_sync(kFull, grow)) {
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
@@ -448,13 +465,11 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) few_kernel(const __grid_con
     st.cells = min(cells, ROWS);
     st.key0 = key0;
     st.key1 = key1;
-    st.low = lo_min;
-    st.high = hi_max;
     st.cluster = f.cluster;
     st.part = part;
     st.whole = !f.cluster && x == u0 && min(x1, u1) == u1;
     st.slot = f.cluster ? nullptr : f.w.part + (2 * (int64_t)part + (x == start ? 0 : 1)) * (int64_t)ROWS * (2 + D);
-    settle<T, D, ROWS, C::PITCH, kFewWarps>(a, st, ml, reinterpret_cast<float*>(smem), kRing / 4, unit_m, bad);
+    settle<T, D, ROWS, C::PITCH, kFewWarps>(a, st, ml, reinterpret_cast<float*>(smem), kRing / 4, unit_m, again);
     if (f.cluster) return;
     sc::fence_proxy_async();           // the numerators were written where the next loads go
     __syncthreads();

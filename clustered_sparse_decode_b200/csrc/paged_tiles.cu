@@ -285,53 +285,64 @@ __device__ __forceinline__ bool next_item(const Tiles& f, Walk& w, Item& it) {
   return true;
 }
 
-// A warp's rows with a finite sum and a numerator that is not (sum_again), out of
-// line: they are rare and need registers.  `rows`: the lanes of such rows; tO, i, hq,
-// m, l: this lane's numerators and row; the keys [k0, k1) went into the products.
-// `slot`: of the partial result, at this warp's first row, or null.  A row that sees
-// no key is 0.
+// A warp's rows whose sum is not NaN and whose numerator is not finite (mend_rows),
+// out of line: they are rare and need registers.  `rows`: the lanes of such rows; i,
+// hq, m, l: this lane's row; the keys [k0, k1) went into the products.  `slot`, `num`:
+// the partial results' maximum and numerator of this warp's first row, or slot null.
 template <typename T, int D>
-__device__ __noinline__ void rows_again(const Attend& a, int b, const Request r, int tile0, int tile, uint32_t rows,
-                                        uint32_t tO, int i, int hq, float m, float l, int k0, int k1, float* slot,
-                                        float* num, int* turns) {
+__device__ __noinline__ void rows_again(const Attend& a, int b, const Request r, int tile0, int tile, uint32_t rows, int i,
+                                        int hq, float m, float l, int k0, int k1, float* slot, float* num, int* turns) {
+  constexpr int E = D / 32;
   const int lane = threadIdx.x & 31, prefix = prefix_of(a, b), h = __shfl_sync(kFull, hq, __ffs(rows) - 1) / a.G;
-  int low, high;
+  int low, high, common[E] = {};
   seen_by(a, r, prefix, tile0, min(r.n, tile0 + tile), low, high);
-  k1 = min(k1, r.len);
-  const int any = odd_values<T, D>(a, b, h, k1, k1, k0, k1, low, high, turns);
-  bool large = false;
-#pragma unroll 1
-  for (int k = 0; k < D; k += 32) {
-    float o[32];
-    tmem_ld(tO + k, o);
-    tmem_ld_wait(o);
+  // the keys that all of these rows see
+  const bool mine = (rows >> lane & 1u) && l > 0.f;
+  const Interval v = interval_of(a, r, prefix, mine ? i : 0);
+  const int c0 = __reduce_max_sync(kFull, mine ? max(v.lo, k0) : k0),
+            c1 = max(c0, __reduce_min_sync(kFull, mine ? min(v.hi, k1) : k1));
+  if (__any_sync(kFull, mine)) odd_values<T, D>(a, b, h, c0, c1, low, high, common, turns);
+  const uint32_t none = __ballot_sync(kFull, l == 0.f);
+  auto result = [&](int hr, int ir) {
+    return reinterpret_cast<T*>(a.O + (int64_t)(r.row0 + ir) * a.o_row_b + (int64_t)hr * a.o_head_b) + lane * E;
+  };
+  for (uint32_t x = rows & none; x; x &= x - 1) {          // zeros (a part that saw nothing: its numerator is not used)
+    const int src = __ffs(x) - 1, ri = __shfl_sync(kFull, i, src), rh = __shfl_sync(kFull, hq, src);
+    if (!slot)
 #pragma unroll
-    for (int q = 0; q < 32; ++q) large |= fabsf(o[q]) > 3.4028235e38f;
+      for (int e = 0; e < E; ++e) result(rh, ri)[e] = from_f32<T>(0.f);
   }
-  const uint32_t inf = __ballot_sync(kFull, large), none = __ballot_sync(kFull, l == 0.f);
-  for (; rows; rows &= rows - 1) {
-    const int src = __ffs(rows) - 1, ri = __shfl_sync(kFull, i, src), rh = __shfl_sync(kFull, hq, src);
-    const float base = __shfl_sync(kFull, m + log2f(l), src);
-    const Interval v = interval_of(a, r, prefix, ri);
-    float s[D / 32] = {};
-    if (none >> src & 1u) {
-      if (slot) continue;
-    } else {
-      const int unseen = any == V_NAN ? odd_values<T, D>(a, b, h, v.lo, v.hi, k0, k1, low, high, turns) : 0;
-      if (!sum_again(any, inf >> src & 1u, unseen)) continue;
-      row_sum<T, D>(a, b, r, ri, rh, k0, k1, base, s, turns);
+  rows &= ~none;
+  while (rows) {
+    Rows4 four;
+    int src[4];
+    float s[4][E] = {};
+    four.n = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (!rows) continue;
+      src[k] = __ffs(rows) - 1;
+      rows &= rows - 1;
+      four.i[k] = __shfl_sync(kFull, i, src[k]);
+      four.hq[k] = __shfl_sync(kFull, hq, src[k]);
+      four.base[k] = __shfl_sync(kFull, m + log2f(l), src[k]);
+      four.n = k + 1;
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        s[k][e] = slot ? num[src[k] * D + lane * E + e] : to_f32(result(four.hq[k], four.i[k])[e]);
     }
-    if (slot) {
-      if (lane == 0) {
-        slot[src] = base;
-        slot[2 * kHalf + src] = 1.f;
+    const uint32_t again = mend_rows<T, D>(a, b, r, four, k0, k1, low, high, c0, c1, common, s, turns);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k >= four.n) continue;
+      if (slot && (again >> k & 1u) && lane == 0) {
+        slot[src[k]] = four.base[k];
+        slot[2 * kHalf + src[k]] = 1.f;
       }
 #pragma unroll
-      for (int e = 0; e < D / 32; ++e) num[src * D + lane * (D / 32) + e] = s[e];
-    } else {
-      T* o = reinterpret_cast<T*>(a.O + (int64_t)(r.row0 + ri) * a.o_row_b + (int64_t)rh * a.o_head_b) + lane * (D / 32);
-#pragma unroll
-      for (int e = 0; e < D / 32; ++e) o[e] = from_f32<T>(s[e]);
+      for (int e = 0; e < E; ++e)
+        if (slot) num[src[k] * D + lane * E + e] = s[k][e];
+        else result(four.hq[k], four.i[k])[e] = from_f32<T>(s[k][e]);
     }
   }
 }
@@ -743,6 +754,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
             *reinterpret_cast<float4*>(num + k + q) = make_float4(o[q], o[q + 1], o[q + 2], o[q + 3]);
         }
       }
+      tc_before();
       if (valid) {
         if (it.whole) {
           if (a.lse)
@@ -755,9 +767,8 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
       const uint32_t again = __ballot_sync(kFull, valid && !finite && l == l);       // (not where the sum is NaN)
       __syncwarp();                    // what the rows' own threads have written is there before another overwrites it
       if (again)
-        rows_again<T, D>(a, it.b, it.r, it.i0, f.tile, again, tO, i, hq, m - kLift<T>, l, it.key0 + it.from[g] * kKeys,
+        rows_again<T, D>(a, it.b, it.r, it.i0, f.tile, again, i, hq, m - kLift<T>, l, it.key0 + it.from[g] * kKeys,
                          it.key0 + it.to[g] * kKeys, it.whole ? nullptr : slot + cell - lane, num - (int64_t)lane * D, turns);
-      tc_before();
       if (it.to[0] > it.from[0] || it.to[1] > it.from[1]) n_kv += 2 * it.nb;
     }
   } else {

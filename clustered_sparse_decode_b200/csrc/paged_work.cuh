@@ -103,11 +103,17 @@ __device__ __forceinline__ void span_of(const Attend& a, const Request& r, int b
 // the scratch, or, in a cluster that shares the unit, the cluster's result.
 struct Settle {
   int b, h, i0, cells, key0, key1;     // request, KV head, first token, (token, head) rows, keys
-  int low, high;                       // keys that its rows see together
   Request r;
   int cluster, part;                   // blocks of the cluster (0: none), this block's place
   bool whole;                          // the unit is this block's alone
   float* slot;                         // of a partial result
+};
+// Shared words that settle needs: rows to be looked at again, and the keys that the
+// unit's rows see together (written before its keys are worked on: there they cost
+// no registers).
+template <int ROWS>
+struct Again {
+  int bad[ROWS], low, high;
 };
 template <typename T>
 __device__ __forceinline__ void settle_final(const Attend& a, const Settle& s, int row, int c, float m, float l, float v) {
@@ -129,38 +135,73 @@ __device__ __forceinline__ void settle_put(const Attend& a, const Settle& s, flo
     if (c == 0) { s.slot[row] = m; s.slot[ROWS + row] = l; }
   }
 }
-// Rows with a finite sum and a numerator that is not (sum_again): out of line, for the registers' sake.
+// Rows with a finite sum and a numerator that is not (mend_rows): out of line, for the registers' sake.
 template <typename T, int D, int ROWS, int PITCH, int WARPS>
-__device__ __noinline__ void settle_again(const Attend& a, const Settle s, const float* ml, float* num, float* unit,
-                                          const int* bad) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int end = min((s.key1 + 15) & ~15, s.r.len);         // of the 16-key tiles
-  const int part = ((end - s.key0 + WARPS - 1) / WARPS + 15) & ~15, k0 = s.key0 + warp * part, k1 = min(k0 + part, end);
-  const int odd = odd_values<T, D>(a, s.b, s.h, k1, k1, k0, k1, s.low, s.high, nullptr);
-  const int any = (__syncthreads_or(odd & V_NAN) ? V_NAN : 0) | (__syncthreads_or(odd & V_INF) ? V_INF : 0);
-  for (int row = warp; row < s.cells; row += WARPS) {
-    if (!bad[row]) continue;
-    const int i = s.i0 + row / a.G;
-    const Interval x = interval_of(a, s.r, prefix_of(a, s.b), i);
-    const int unseen = any == V_NAN ? odd_values<T, D>(a, s.b, s.h, x.lo, x.hi, s.key0, end, s.low, s.high, nullptr) : 0;
-    if (!sum_again(any, bad[row] & V_INF, unseen)) continue;
-    float m = -INFINITY, l = 0.f, v[D / 32];
-    for (int w = 0; w < WARPS; ++w) m = fmaxf(m, ml[(w * 2) * ROWS + row]);
-    for (int w = 0; w < WARPS; ++w) {
-      const float mw = ml[(w * 2) * ROWS + row];
-      l = fmaf(mw == -INFINITY ? 0.f : exp2f(mw - m), ml[(w * 2 + 1) * ROWS + row], l);
+__device__ __noinline__ void settle_again(const Attend& a, const Settle& s, const float* ml, float* num, int stride,
+                                          float* unit, const Again<ROWS>* again) {
+  constexpr int E = D / 32;
+  const int* bad = again->bad;
+  const int low = again->low, high = again->high;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, prefix = prefix_of(a, s.b);
+  // the keys that all of this warp's rows see
+  int c0 = s.key0, c1 = s.key1, common[E] = {};
+  bool any = false;
+  for (int row = warp; row < s.cells; row += WARPS)
+    if (bad[row]) {
+      const Interval v = interval_of(a, s.r, prefix, s.i0 + row / a.G);
+      c0 = max(c0, v.lo);
+      c1 = min(c1, v.hi);
+      any = true;
     }
-    m += log2f(l);
-    row_sum<T, D>(a, s.b, s.r, i, s.h * a.G + row % a.G, s.key0, s.key1, m, v, nullptr);
+  if (!any) return;
+  c1 = max(c0, c1);
+  odd_values<T, D>(a, s.b, s.h, c0, c1, low, high, common, nullptr);
+  for (int next = warp; next < s.cells;) {
+    Rows4 rows;
+    int row[4];
+    float m[4], l[4], v[4][E] = {};
+    rows.n = 0;
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) settle_put<T, D, ROWS, PITCH>(a, s, num, unit, row, lane * (D / 32) + e, m, 1.f, v[e]);
+    for (int k = 0; k < 4; ++k) {
+      while (next < s.cells && !bad[next]) next += WARPS;
+      if (next >= s.cells) continue;
+      row[k] = next;
+      m[k] = -INFINITY;
+      l[k] = 0.f;
+      for (int w = 0; w < WARPS; ++w) m[k] = fmaxf(m[k], ml[(w * 2) * ROWS + next]);
+      for (int w = 0; w < WARPS; ++w) {
+        const float mw = ml[(w * 2) * ROWS + next], f = mw == -INFINITY ? 0.f : exp2f(mw - m[k]);
+        l[k] = fmaf(f, ml[(w * 2 + 1) * ROWS + next], l[k]);
+#pragma unroll
+        for (int e = 0; e < E; ++e)    // (in a cluster the first warp's have been replaced by the sum)
+          if (!s.cluster) v[k][e] = fmaf(f, num[w * stride + next * PITCH + lane * E + e], v[k][e]);
+          else if (w == 0) v[k][e] = num[next * PITCH + lane * E + e];
+      }
+      rows.i[k] = s.i0 + next / a.G;
+      rows.hq[k] = s.h * a.G + next % a.G;
+      rows.base[k] = m[k] + log2f(l[k]);
+      rows.n = k + 1;
+      next += WARPS;
+    }
+    if (rows.n == 0) break;
+    const uint32_t summed = mend_rows<T, D>(a, s.b, s.r, rows, s.key0, s.key1, low, high, c0, c1, common, v, nullptr);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k >= rows.n) continue;
+      const bool one = summed >> k & 1u;
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        settle_put<T, D, ROWS, PITCH>(a, s, num, unit, row[k], lane * E + e, one ? rows.base[k] : m[k], one ? 1.f : l[k],
+                                      v[k][e]);
+    }
   }
 }
 template <typename T, int D, int ROWS, int PITCH, int WARPS>
-__device__ void settle(const Attend& a, const Settle& s, const float* ml, float* num, int stride, float* unit, int* bad) {
+__device__ void settle(const Attend& a, const Settle& s, const float* ml, float* num, int stride, float* unit,
+                       Again<ROWS>* again) {
   namespace cg = cooperative_groups;
   const int tid = threadIdx.x;
-  if (tid < ROWS) bad[tid] = 0;
+  if (tid < ROWS) again->bad[tid] = 0;
   __syncthreads();
   bool mine = false;
   for (int row = tid / D; row < s.cells; row += WARPS * 32 / D) {
@@ -175,12 +216,12 @@ __device__ void settle(const Attend& a, const Settle& s, const float* ml, float*
       v = fmaf(k, num[w * stride + row * PITCH + c], v);
     }
     if (!isfinite(v) && isfinite(l) && l > 0.f) {
-      atomicOr(bad + row, v != v ? V_NAN : V_INF);
+      again->bad[row] = 1;
       mine = true;
     }
     settle_put<T, D, ROWS, PITCH>(a, s, num, unit, row, c, m, l, v);
   }
-  if (__syncthreads_or(mine)) settle_again<T, D, ROWS, PITCH, WARPS>(a, s, ml, num, unit, bad);
+  if (__syncthreads_or(mine)) settle_again<T, D, ROWS, PITCH, WARPS>(a, s, ml, num, stride, unit, again);
   if (!s.cluster) return;
   cg::cluster_group cl = cg::this_cluster();
   cl.sync();

@@ -27,10 +27,12 @@ def test_rows_done_again_are_the_ones_that_stay(dtype, d, n, new):
 @pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f16", 64), ("f32", 64)])
 @pytest.mark.parametrize("new", [1, 6, 300])
 @pytest.mark.parametrize("kind", ["one_value", "all_behind"])
-def test_bad_values_of_one_request_stay_its_own(dtype, d, new, kind):
+@pytest.mark.parametrize("qscale", [1.0, 20.0])
+def test_bad_values_of_one_request_stay_its_own(dtype, d, new, kind, qscale):
     """An early NaN and a late infinity among one long request's values: in its own rows where they belong, in the
-    columns that hold them, and nowhere else; other requests' rows are written as without it."""
-    c = Case([16400, 16400, 700], [new] * 3, H=1, G=4, d=d, P=64, dtype=dtype, seed=31)
+    columns that hold them, and nowhere else, however small their weights; other requests' rows are written as without
+    it."""
+    c = Case([16400, 16400, 700], [new] * 3, H=1, G=4, d=d, P=64, dtype=dtype, seed=31, qscale=qscale)
     want = c.want()
     tol, ltol = bounds(c, want[2], want[0], want[1])
     late = 16400 - min(50, new // 2 + 1)
