@@ -891,12 +891,14 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
                     it.r.row0 + it.i0 + g * (f.tile / 2), q_full + 8 * qb);
         }
         for (int j = 0; j < it.nb && ok; ++j) {
-          // a lane a box: its keys' page (page 0 in the place of a bad one, whose result does not count; a neighbour
-          // that is seen in the place of one that is not, whose table entry need not be valid any more)
+          // a lane a box: its keys' page (a page behind the pool's last, which reads as zeros, in the place of a bad one,
+          // so that nothing of another request is read; a neighbour that is seen in the place of one that is not, whose
+          // table entry need not be valid any more)
           const int key = it.key0 + j * kKeys + lane * f.box;
           const bool mine = lane < boxes && key < it.r.len;
           const int known = min(max(key, it.lo), it.hi - 1);
-          const int page = mine ? max(0, page_of(a, it.b, known)) : 0;
+          int page = mine ? page_of(a, it.b, known) : 0;
+          if (page < 0) page = a.num_pages;
           const uint32_t bytes = __popc(__ballot_sync(kFull, mine)) * (uint32_t)f.box * D * 2;
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {

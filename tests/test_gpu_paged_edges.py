@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 import torch
 
-from paged_cases import TDT, Case, bounds, cache_of, call
+from paged_cases import TDT, Case, bounds, cache_of, call, dev
 
 pytestmark = pytest.mark.gpu
 
@@ -65,3 +65,30 @@ def test_values_near_the_types_largest(dtype, new):
     tol = bounds(c, want[2], want[0], want[1])[0]
     assert np.isfinite(got[0]).all()
     assert (np.abs(got[0] - want[0]) <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("P", [16, 64, 256])
+@pytest.mark.parametrize("new", [1, 4, 40, 300])
+def test_a_bad_page_is_nobody_elses(dtype, P, new):
+    """What a request with a bad table entry gets comes from no other page, and other requests' rows stay."""
+    c = Case([700, 700, 350], [new] * 3, H=2, G=4, d=64, P=P, dtype=dtype, seed=5)
+    want = c.want()
+    tol = bounds(c, want[2], want[0], want[1])[0]
+    table = c.table.copy()
+    table[0, 1], table[1, 0] = c.pages, -1
+    mine = set(table[:2].ravel()) | set(c.table[2].ravel())
+    for p in range(c.pages):
+        if p not in mine:
+            c.K[p], c.V[p] = 1.0, 1000.0
+    # whatever page stands first in the pool is one of these
+    z = next(p for p in range(c.pages) if p not in mine)
+    order = np.arange(c.pages)
+    order[[0, z]] = z, 0
+    c.K, c.V = c.K[order], c.V[order]
+    moved = np.where(table == 0, z, np.where(table == z, 0, table))
+    cache = cache_of(c)
+    out = cache.attend(dev(c.Q, dtype), dev(moved), dev(c.lens), dev(c.cu), max_new=new).double().cpu().numpy()
+    assert cache.check_device_error() == 1
+    assert np.abs(out[:2 * new]).max() < 10
+    assert (np.abs(out[2 * new:] - want[0][2 * new:]) <= tol[2 * new:]).all()
