@@ -219,7 +219,8 @@ struct Gather {
 __global__ void __launch_bounds__(kCopyThreads) gather_kernel(const Gather a) {
   const int chunk = (int)(blockIdx.x % (unsigned)a.chunks), bh = (int)(blockIdx.x / (unsigned)a.chunks);
   const int b = bh / a.H, h = bh - b * a.H;
-  const int len = min((int64_t)max(__ldg(a.lens + b), 0), (int64_t)a.table_pages << a.page_shift);
+  const int held = __ldg(a.lens + b), len = min((int64_t)max(held, 0), (int64_t)a.table_pages << a.page_shift);
+  if (len != held && threadIdx.x == 0) set_error(a.err, E_BAD_OFFSET);
   const int vec = threadIdx.x & ((1 << a.vshift) - 1), r0 = threadIdx.x >> a.vshift, dr = kCopyThreads >> a.vshift;
   const int end = min(a.n, (chunk + 1) * kGatherRows);
   const int64_t out0 = (int64_t)bh * a.n;

@@ -404,7 +404,8 @@ mp_status mp_paged_attend_scratch(const mp_paged_cache* cache, const mp_paged_at
 
 /* Copy the tokens [0, n) of every request into K_out, V_out, contiguous
  * [batch, kv_heads, n, head_dim]: what mp_cluster_build takes.  Rows from
- * lens[b] on are zero.  n <= table_pages * page_tokens. */
+ * lens[b] on are zero.  n <= table_pages * page_tokens.  A length below 0 or past
+ * the table sets bit 1 and counts as the nearest one that is not. */
 mp_status mp_paged_gather(const mp_paged_cache* cache, int32_t batch, const int32_t* table, int32_t table_pages,
                           int32_t table_stride, const int32_t* lens, int32_t n, void* K_out, void* V_out,
                           void* stream);

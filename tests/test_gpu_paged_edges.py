@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import paged as op
 from paged_cases import TDT, Case, bounds, cache_of, call, dev
 
 pytestmark = pytest.mark.gpu
@@ -92,3 +93,14 @@ def test_a_bad_page_is_nobody_elses(dtype, P, new):
     assert cache.check_device_error() == 1
     assert np.abs(out[:2 * new]).max() < 10
     assert (np.abs(out[2 * new:] - want[0][2 * new:]) <= tol[2 * new:]).all()
+
+
+@pytest.mark.parametrize("lens", [[-1, 40], [20, 65], [20, 1 << 30]])
+def test_gather_flags_lengths_outside_the_table(lens):
+    c = Case([20, 64], [0, 0], H=1, G=1, d=64)
+    cache = cache_of(c)
+    n = 30
+    K, _ = cache.gather(dev(c.table), dev(lens), n)
+    held = [min(max(m, 0), 64) for m in lens]
+    assert np.array_equal(K.double().cpu().numpy(), op.gather(c.K, c.table, held, n, 16))
+    assert cache.check_device_error() == 1
