@@ -18,7 +18,7 @@ EXPORTS = ["mp_workspace_size", "mp_index_init", "mp_cluster_build", "mp_cluster
            "mp_decode_static",
            "mp_index_export", "mp_index_import", "mp_check_device_error", "mp_decode_phases", "mp_status_str",
            "mp_paged_init", "mp_paged_plan", "mp_paged_append", "mp_paged_attend", "mp_paged_attend_scratch",
-           "mp_paged_gather", "mp_paged_check_error"]
+           "mp_paged_gather", "mp_paged_gather_whole", "mp_paged_check_error"]
 
 
 class MpConfig(ctypes.Structure):
@@ -125,6 +125,7 @@ def load():
         "mp_paged_attend": [vp, ctypes.c_char_p, vp, sz, vp],
         "mp_paged_attend_scratch": [vp, ctypes.c_char_p, P(sz)],
         "mp_paged_gather": [vp, i32, vp, i32, i32, vp, i32, vp, vp, vp],
+        "mp_paged_gather_whole": [vp, i32, vp, i32, i32, vp, i32, vp, vp, vp],
         "mp_paged_check_error": [vp, P(i32), vp],
     }
     for name, args in sig.items():

@@ -172,9 +172,10 @@ class MultipoleIndex:
         """Cluster the first n tokens of the paged cache's requests from scratch.
 
         cache: a PagedCache of this index's heads, head_dim and dtype; table,
-        lens: its block table and lengths, one request per sequence of the batch
-        (a request shorter than n contributes zero rows).  Gathers the pages
-        (mp_paged_gather) and builds (mp_cluster_build).
+        lens: its block table and lengths, one request per sequence of the batch.
+        Gathers the pages (mp_paged_gather_whole) and builds (mp_cluster_build).
+        The index holds n tokens of each: a request shorter than n sets the
+        cache's error word, and its missing tokens are zero rows.
         """
         c = self.cfg
         if (cache.kv_heads, cache.head_dim, cache.torch_dtype) != (c.kv_heads, c.head_dim, c.torch_dtype):
@@ -183,7 +184,7 @@ class MultipoleIndex:
             raise ValueError(f"the index holds {c.batch} sequences on {self.device}")
         if not 0 <= n <= c.max_tokens:
             L.check(L.MP_ENOSPC if n > 0 else L.MP_EINVAL, "build_paged")
-        K, V = cache.gather(table, lens, n, stream=stream)
+        K, V = cache.gather(table, lens, n, whole=True, stream=stream)
         self.build(K, V, stream=stream)
 
     def update(self, K_new, V_new, stream=None):

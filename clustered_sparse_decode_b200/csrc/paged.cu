@@ -213,6 +213,7 @@ struct Gather {
   const int32_t* table;
   const int32_t* lens;
   int32_t table_pages, table_stride, num_pages, page_shift, H, n, vshift, chunks;
+  int32_t least;                         // tokens that a request has to hold
   int32_t* err;
 };
 
@@ -220,7 +221,7 @@ __global__ void __launch_bounds__(kCopyThreads) gather_kernel(const Gather a) {
   const int chunk = (int)(blockIdx.x % (unsigned)a.chunks), bh = (int)(blockIdx.x / (unsigned)a.chunks);
   const int b = bh / a.H, h = bh - b * a.H;
   const int held = __ldg(a.lens + b), len = min((int64_t)max(held, 0), (int64_t)a.table_pages << a.page_shift);
-  if (len != held && threadIdx.x == 0) set_error(a.err, E_BAD_OFFSET);
+  if ((len != held || held < a.least) && threadIdx.x == 0) set_error(a.err, E_BAD_OFFSET);
   const int vec = threadIdx.x & ((1 << a.vshift) - 1), r0 = threadIdx.x >> a.vshift, dr = kCopyThreads >> a.vshift;
   const int end = min(a.n, (chunk + 1) * kGatherRows);
   const int64_t out0 = (int64_t)bh * a.n;
@@ -441,8 +442,9 @@ mp_status mp_paged_append(const mp_paged_cache* c, const void* K_new, const void
   return launched();
 }
 
-mp_status mp_paged_gather(const mp_paged_cache* c, int32_t batch, const int32_t* table, int32_t table_pages,
-                          int32_t table_stride, const int32_t* lens, int32_t n, void* K_out, void* V_out, void* stream) {
+static mp_status gather(const mp_paged_cache* c, int32_t batch, const int32_t* table, int32_t table_pages,
+                        int32_t table_stride, const int32_t* lens, int32_t n, int32_t least, void* K_out, void* V_out,
+                        void* stream) {
   if (!c || batch < 0 || n < 0 || table_pages < 0 || table_stride < table_pages) return MP_EINVAL;
   if (n > (int64_t)table_pages * c->cfg.page_tokens) return MP_EINVAL;
   if (batch > 0 && n > 0 && (!table || !lens || !K_out || !V_out)) return MP_EINVAL;
@@ -469,11 +471,23 @@ mp_status mp_paged_gather(const mp_paged_cache* c, int32_t batch, const int32_t*
   a.n = n;
   a.vshift = log2_of(c->cfg.head_dim * es / 16);
   a.chunks = (n - 1) / kGatherRows + 1;
+  a.least = least;
   a.err = c->err;
   const int64_t grid = (int64_t)batch * a.H * a.chunks;
   if (grid > INT32_MAX) return MP_EUNSUPPORTED;
   gather_kernel<<<(unsigned)grid, kCopyThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
   return launched();
+}
+
+mp_status mp_paged_gather(const mp_paged_cache* c, int32_t batch, const int32_t* table, int32_t table_pages,
+                          int32_t table_stride, const int32_t* lens, int32_t n, void* K_out, void* V_out, void* stream) {
+  return gather(c, batch, table, table_pages, table_stride, lens, n, 0, K_out, V_out, stream);
+}
+
+mp_status mp_paged_gather_whole(const mp_paged_cache* c, int32_t batch, const int32_t* table, int32_t table_pages,
+                                int32_t table_stride, const int32_t* lens, int32_t n, void* K_out, void* V_out,
+                                void* stream) {
+  return gather(c, batch, table, table_pages, table_stride, lens, n, n, K_out, V_out, stream);
 }
 
 static mp_status check_attend(const mp_paged_cache* c, const mp_paged_attend_args* p) {

@@ -213,11 +213,13 @@ class PagedCache:
         self._run(stream, "mp_paged_attend", self.lib.mp_paged_attend, self._h, args, s, n)
         return out
 
-    def gather(self, table, lens, n, out=None, stream=None):
+    def gather(self, table, lens, n, out=None, stream=None, whole=False):
         """The first n tokens of every request as K, V [B, kv_heads, n, head_dim] (mp_paged_gather).
 
         The layout that MultipoleIndex.build and dense_decode take; rows from
-        lens[b] on are zero.  out: (K, V) to write to.
+        lens[b] on are zero.  whole: every request has to hold n tokens, a
+        shorter one sets the cache's error word (mp_paged_gather_whole).  out:
+        (K, V) to write to.
         """
         B, W, stride = self._table(table)
         shape = (B, self.kv_heads, n, self.head_dim)
@@ -229,7 +231,8 @@ class PagedCache:
             for t in (K, V):
                 if t.shape != shape or t.dtype is not self.torch_dtype or t.device != self.device or not t.is_contiguous():
                     raise ValueError(f"out must be contiguous {self.torch_dtype} tensors of shape {shape} on {self.device}")
-        self._run(stream, "mp_paged_gather", self.lib.mp_paged_gather, self._h, B, table.data_ptr(), W, stride,
+        f = self.lib.mp_paged_gather_whole if whole else self.lib.mp_paged_gather
+        self._run(stream, f.__name__, f, self._h, B, table.data_ptr(), W, stride,
                   self._ints(lens, B, "lens"), n, K.data_ptr(), V.data_ptr())
         return K, V
 

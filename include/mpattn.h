@@ -410,6 +410,13 @@ mp_status mp_paged_gather(const mp_paged_cache* cache, int32_t batch, const int3
                           int32_t table_stride, const int32_t* lens, int32_t n, void* K_out, void* V_out,
                           void* stream);
 
+/* The same for requests that have to hold n tokens, as those that a clustering
+ * takes (it would attend a shorter one's zero rows like tokens): a length below n
+ * sets bit 1 too. */
+mp_status mp_paged_gather_whole(const mp_paged_cache* cache, int32_t batch, const int32_t* table, int32_t table_pages,
+                                int32_t table_stride, const int32_t* lens, int32_t n, void* K_out, void* V_out,
+                                void* stream);
+
 /* mp_check_device_error for a paged cache: synchronises `stream`, reads and
  * clears the error word. */
 mp_status mp_paged_check_error(const mp_paged_cache* cache, int32_t* code, void* stream);

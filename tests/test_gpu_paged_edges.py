@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 import torch
 
+from clustered_sparse_decode_b200 import Config, MultipoleIndex
 from oracle import paged as op
 from paged_cases import TDT, Case, bounds, cache_of, call, dev
 
@@ -104,3 +105,14 @@ def test_gather_flags_lengths_outside_the_table(lens):
     held = [min(max(m, 0), 64) for m in lens]
     assert np.array_equal(K.double().cpu().numpy(), op.gather(c.K, c.table, held, n, 16))
     assert cache.check_device_error() == 1
+
+
+def test_build_paged_flags_requests_shorter_than_n():
+    c = Case([64, 50], [0, 0], H=1, G=1, d=64)
+    cfg = Config(batch=2, kv_heads=1, q_heads=1, head_dim=64, max_tokens=64, block_tokens=64, kmeans_iters=1)
+    cache, idx = cache_of(c), MultipoleIndex(cfg)
+    idx.build_paged(cache, dev(c.table), dev(c.lens), 50)
+    assert cache.check_device_error() == 0
+    idx.build_paged(cache, dev(c.table), dev(c.lens), 51)
+    assert cache.check_device_error() == 1
+    assert idx.check_device_error() == 0
