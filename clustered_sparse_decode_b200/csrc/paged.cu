@@ -490,6 +490,27 @@ mp_status mp_paged_gather_whole(const mp_paged_cache* c, int32_t batch, const in
   return gather(c, batch, table, table_pages, table_stride, lens, n, n, K_out, V_out, stream);
 }
 
+// Whether two of the d-element rows at i row + j head, |i| < rows, |j| < heads, can
+// be less than d elements apart, the second set `shift` elements behind the first
+// (0: one set, and a row is not compared with itself).
+static bool rows_meet(int64_t shift, int64_t rows, int64_t heads, int64_t row, int64_t head, int64_t d) {
+  using wide = __int128;
+  if (rows == 1) row = 0;
+  if (heads == 1) head = 0;
+  if (shift == 0 && (row >= (wide)(heads - 1) * head + d || rows == 1) && (head >= d || heads == 1)) return false;
+  if (shift == 0 && (head >= (wide)(rows - 1) * row + d || heads == 1) && (row >= d || rows == 1)) return false;
+  for (int64_t j = 1 - heads; j < heads; ++j) {
+    const wide at = (wide)shift + (wide)j * head;
+    const wide near = row > 0 ? -at / row : 0;           // the i that brings the two rows nearest, or its neighbour
+    for (wide i = near - 1; i <= near + 1; ++i) {
+      if (i <= -rows || i >= rows || (shift == 0 && i == 0 && j == 0)) continue;
+      const wide apart = at + i * row;
+      if (apart < d && apart > -d) return true;
+    }
+  }
+  return false;
+}
+
 static mp_status check_attend(const mp_paged_cache* c, const mp_paged_attend_args* p) {
   if (!c || !p) return MP_EINVAL;
   const mp_paged_config& g = c->cfg;
@@ -506,7 +527,6 @@ static mp_status check_attend(const mp_paged_cache* c, const mp_paged_attend_arg
     if (p->q_heads > 1 && (heads_st[i] < 0 || (heads_st[i] * es) % 16 != 0)) return MP_EINVAL;
   }
   if ((reinterpret_cast<uintptr_t>(p->Q) | reinterpret_cast<uintptr_t>(p->O)) % 16 != 0) return MP_EINVAL;
-  // rows of O that fall on one another would be written by several blocks
   if ((p->rows > 1 && p->o_row_stride < g.head_dim) || (p->q_heads > 1 && p->o_head_stride < g.head_dim)) return MP_EINVAL;
   if (!std::isfinite(p->scale) || !std::isfinite(p->softcap) || p->softcap < 0.f || p->window < 0 ||
       (p->flags & ~MP_ATTEND_FULL) != 0)
@@ -515,6 +535,9 @@ static mp_status check_attend(const mp_paged_cache* c, const mp_paged_attend_arg
   if ((G != 1 && G != 2 && G != 4 && G != 8) || p->batch > 65535 || p->rows > (1 << 24) ||
       (int64_t)p->table_pages * g.page_tokens > (1 << 30))
     return MP_EUNSUPPORTED;
+  // rows of O that fall on one another would be written by several blocks
+  if (p->batch > 0 && p->rows > 0 && rows_meet(0, p->rows, p->q_heads, p->o_row_stride, p->o_head_stride, g.head_dim))
+    return MP_EINVAL;
   return MP_OK;
 }
 
