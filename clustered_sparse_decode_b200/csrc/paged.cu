@@ -511,6 +511,16 @@ static bool rows_meet(int64_t shift, int64_t rows, int64_t heads, int64_t row, i
   return false;
 }
 
+// Whether O's rows meet Q's.  Rows of unlike strides in one another's span count as meeting.
+static bool output_meets_input(const mp_paged_attend_args& p, int d, int es) {
+  const int64_t qr = p.rows > 1 ? p.q_row_stride : 0, qh = p.q_heads > 1 ? p.q_head_stride : 0;
+  const int64_t orow = p.rows > 1 ? p.o_row_stride : 0, oh = p.q_heads > 1 ? p.o_head_stride : 0;
+  const __int128 q0 = reinterpret_cast<uintptr_t>(p.Q), o0 = reinterpret_cast<uintptr_t>(p.O), t = p.rows - 1, h = p.q_heads - 1;
+  if (q0 + (t * qr + h * qh + d) * es <= o0 || o0 + (t * orow + h * oh + d) * es <= q0) return false;
+  if (qr != orow || qh != oh || o0 == q0) return true;
+  return rows_meet((int64_t)(o0 - q0) / es, p.rows, p.q_heads, qr, qh, d);
+}
+
 static mp_status check_attend(const mp_paged_cache* c, const mp_paged_attend_args* p) {
   if (!c || !p) return MP_EINVAL;
   const mp_paged_config& g = c->cfg;
@@ -554,6 +564,8 @@ mp_status mp_paged_attend(const mp_paged_cache* c, const mp_paged_attend_args* p
   mp_status s = check_attend(c, p);
   if (s != MP_OK) return s;
   if (reinterpret_cast<uintptr_t>(d_scratch) % 256 != 0) return MP_EINVAL;
+  // (a row that is done again reads its queries after other rows' results are written)
+  if (p->batch > 0 && p->rows > 0 && output_meets_input(*p, c->cfg.head_dim, elem_bytes16(c->cfg.dtype))) return MP_EINVAL;
   if ((s = check_cache(c)) != MP_OK) return s;
   if (p->batch == 0 || p->rows == 0) return MP_OK;
   const size_t need = paged_attend_scratch_bytes(*c, *p);

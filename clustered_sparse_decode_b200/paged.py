@@ -169,7 +169,7 @@ class PagedCache:
         up to its own position (all with full=True), those before prefix[b], only
         the last `window` positions (0: all), and none before first_key[row].
         Scores are scale * q.k, capped by softcap * tanh(z / softcap), minus
-        slopes[head] * |position - key|.  max_new: most rows that a request has (a
+        slopes[head] * |position - key|.  out must not overlap Q.  max_new: most rows that a request has (a
         bound known to the host; it chooses the kernel).  Returns O [rows, Hq, d];
         rows behind cu[B] are left as they are.  lse: float32 [rows, Hq] that
         receives the log of each row's sum, -inf where it sees nothing.

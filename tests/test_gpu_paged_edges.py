@@ -3,7 +3,8 @@ import numpy as np
 import pytest
 import torch
 
-from clustered_sparse_decode_b200 import Config, MultipoleIndex
+from clustered_sparse_decode_b200 import Config, MpError, MultipoleIndex
+from clustered_sparse_decode_b200 import _lib as L
 from oracle import paged as op
 from paged_cases import TDT, Case, bounds, cache_of, call, dev
 
@@ -116,3 +117,26 @@ def test_build_paged_flags_requests_shorter_than_n():
     idx.build_paged(cache, dev(c.table), dev(c.lens), 51)
     assert cache.check_device_error() == 1
     assert idx.check_device_error() == 0
+
+
+@pytest.mark.parametrize("new", [1, 4, 60])
+def test_queries_and_output_in_one_buffer(new):
+    """Slices of a joined projection that do not overlap are taken, the queries' own place is refused."""
+    c = Case([300, 90], [new, new], H=2, G=2, d=64, P=32, dtype="bf16", seed=17)
+    cache = cache_of(c)
+    buf = torch.zeros(c.rows, 12, 64, dtype=torch.bfloat16, device="cuda")
+    O, lse, info = c.want()
+    tol = bounds(c, info, O, lse)[0]
+    for at in (0, 4, 8):
+        q, out = buf[:, 4:8], buf[:, at:at + 4]
+        q.copy_(dev(c.Q, "bf16"))
+        args = dict(max_new=new, out=out)
+        if at == 4:
+            with pytest.raises(MpError) as e:
+                cache.attend(q, dev(c.table), dev(c.lens), dev(c.cu), **args)
+            assert e.value.status == L.MP_EINVAL
+            continue
+        cache.attend(q, dev(c.table), dev(c.lens), dev(c.cu), **args)
+        assert (np.abs(out.double().cpu().numpy() - O) <= tol).all()
+        assert torch.equal(q, dev(c.Q, "bf16"))
+    assert cache.check_device_error() == 0

@@ -36,6 +36,17 @@ def test_output_rows_do_not_meet(lib, kw, status):   # noqa: F811
     assert lib.mp_paged_attend_scratch(ctypes.byref(cache()), a, ctypes.byref(need)) == status
 
 
+@pytest.mark.parametrize("kw", [
+    dict(O=Q), dict(O=Q + 4 * 512 * 2 - 16), dict(O=Q - 4 * 512 * 2 + 16),
+    # slices of one buffer [4 rows, 24 heads, 64]: the first 8 heads in, others out
+    dict(q_row_stride=1536, o_row_stride=1536, O=Q + 7 * 64 * 2), dict(q_row_stride=1536, o_row_stride=1536, O=Q + 17 * 64 * 2),
+    dict(q_row_stride=1536, o_row_stride=512, O=Q + 8 * 64 * 2),       # unlike strides in Q's span
+    dict(q_row_stride=0, q_head_stride=0, O=Q + 32 * 2),
+])
+def test_output_does_not_meet_the_queries(lib, kw):  # noqa: F811
+    assert lib.mp_paged_attend(ctypes.byref(cache()), attend_args(**{**APART, **kw}), None, 0, None) == L.MP_EINVAL
+
+
 @pytest.mark.parametrize("seed", range(40))
 def test_overlap_by_brute_force(lib, seed):          # noqa: F811
     r = random.Random(seed)
@@ -45,11 +56,14 @@ def test_overlap_by_brute_force(lib, seed):          # noqa: F811
         a.update(o_row_stride=a["q_row_stride"], o_head_stride=a["q_head_stride"])
     else:
         a.update(o_row_stride=8 * r.randint(0, 90), o_head_stride=8 * r.randint(1, 60))
+    shift = 8 * r.randint(-150, 150)
 
     def spots(kind):
         return [t * a[kind + "_row_stride"] * (rows > 1) + h * a[kind + "_head_stride"] for t in range(rows) for h in range(heads)]
-    o = spots("o")
+    q, o = spots("q"), [x + shift for x in spots("o")]
     need = ctypes.c_size_t()
-    args = attend_args(Q=Q, O=O, **a)
+    args = attend_args(Q=Q, O=Q + 2 * shift, **a)
     meets = any(abs(x - y) < 64 for i, x in enumerate(o) for y in o[:i])
     assert lib.mp_paged_attend_scratch(ctypes.byref(cache()), args, ctypes.byref(need)) == (L.MP_EINVAL if meets else L.MP_OK)
+    if meets or any(abs(x - y) < 64 for x in o for y in q):
+        assert lib.mp_paged_attend(ctypes.byref(cache()), args, None, 0, None) == L.MP_EINVAL
