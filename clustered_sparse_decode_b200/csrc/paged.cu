@@ -382,12 +382,6 @@ mp_status mp_paged_plan(const mp_paged_cache* c, const mp_paged_plan_args* p, vo
   const bool in_place = p->lens == p->lens_out || p->free_count == p->free_count_out;
   a.clustered = blocks <= kPlanCluster || in_place;
   const size_t smem = (size_t)(3 * p->batch + 1) * 4;
-  // (the attribute stays set; without more than 40 KB the call would be the dearest part of a step's)
-  if (smem > 40 * 1024 &&
-      cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
-    cudaGetLastError();
-    return MP_ECUDA;
-  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(std::min(blocks, a.clustered ? kPlanCluster : c->sms));
   cfg.blockDim = dim3(threads);
@@ -399,7 +393,11 @@ mp_status mp_paged_plan(const mp_paged_cache* c, const mp_paged_plan_args* p, vo
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = a.clustered ? 1 : 0;
-  if (cudaLaunchKernelEx(&cfg, plan_kernel, (const Plan)a) != cudaSuccess) {
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e = smem > 40 * 1024
+                            ? launch_large(plan_kernel, cfg, a, c->device, allowed, (size_t)(3 * kPlanBatch + 1) * 4)
+                            : cudaLaunchKernelEx(&cfg, plan_kernel, (const Plan)a);
+  if (e != cudaSuccess) {
     cudaGetLastError();
     return MP_ECUDA;
   }

@@ -599,7 +599,7 @@ static cudaError_t launch_f32_t(const F32& f, int units, cudaStream_t st) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   static std::atomic<uint64_t> allowed{0};
-  return launch_large(kern, cfg, f, f.a.device, allowed);
+  return launch_large(kern, cfg, f, f.a.device, allowed, C::SMEM);
 }
 
 template <int D>
@@ -623,7 +623,7 @@ static cudaError_t launch_many(const F32& f, cudaStream_t st) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   static std::atomic<uint64_t> allowed{0};
-  return launch_large(f32_many_kernel<D>, cfg, f, f.a.device, allowed);
+  return launch_large(f32_many_kernel<D>, cfg, f, f.a.device, allowed, C::SMEM);
 }
 
 cudaError_t attend_f32(const Attend& a, const mp_paged_cache& c, const Work& w, int rows, int tile, int cluster,

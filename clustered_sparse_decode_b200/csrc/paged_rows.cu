@@ -498,7 +498,7 @@ static cudaError_t launch_few_t(Few& f, int units, cudaStream_t st) {
   cfg.attrs = attr;
   cfg.numAttrs = f.cluster || f.a.batch > kOwnList ? 1 : 0;
   static std::atomic<uint64_t> allowed{0};
-  return launch_large(kern, cfg, f, f.a.device, allowed);
+  return launch_large(kern, cfg, f, f.a.device, allowed, C::SMEM);
 }
 
 template <typename T, int D>

@@ -950,7 +950,7 @@ static cudaError_t launch_tiles_t(const Tiles& f, cudaStream_t st) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   static std::atomic<uint64_t> allowed{0};
-  return launch_large(kern, cfg, f, f.a.device, allowed);
+  return launch_large(kern, cfg, f, f.a.device, allowed, C::SMEM);
 }
 
 template <typename T, int D>

@@ -316,16 +316,17 @@ cudaError_t attend_tiles(const Attend& a, const mp_paged_cache& c, const Work& w
 // Launches a kernel that needs more shared memory than the default.  The
 // permission costs about as much as a launch and stays with the device's
 // context, so it is asked for once a device, and again if a launch is refused
-// (the context may be a new one).
+// (the context may be a new one).  It is for the most that any call of the kernel
+// needs (`most`), so that calls from several threads do not take it from another.
 template <typename Kernel, typename Args>
 inline cudaError_t launch_large(Kernel* kernel, const cudaLaunchConfig_t& cfg, const Args& args, int device,
-                                std::atomic<uint64_t>& done) {
+                                std::atomic<uint64_t>& done, size_t most) {
   const uint64_t bit = device < 64 ? (uint64_t)1 << device : 0;
   const bool had = (done.load(std::memory_order_relaxed) & bit) != 0;
   for (int turn = had ? 1 : 0;; ++turn) {
     if (turn != 1 || !had) {
       const cudaError_t e =
-          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
+          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
       if (e != cudaSuccess) return e;
       done.fetch_or(bit, std::memory_order_relaxed);
     }

@@ -1,9 +1,11 @@
 """Paged-cache calls at the edges of what their documentation allows."""
+import threading
+
 import numpy as np
 import pytest
 import torch
 
-from clustered_sparse_decode_b200 import Config, MpError, MultipoleIndex
+from clustered_sparse_decode_b200 import Config, MpError, MultipoleIndex, PagedCache
 from clustered_sparse_decode_b200 import _lib as L
 from oracle import paged as op
 from paged_cases import TDT, Case, bounds, cache_of, call, dev
@@ -140,3 +142,56 @@ def test_queries_and_output_in_one_buffer(new):
         assert (np.abs(out.double().cpu().numpy() - O) <= tol).all()
         assert torch.equal(q, dev(c.Q, "bf16"))
     assert cache.check_device_error() == 0
+
+
+def many_requests(B, P=16):
+    """A step of B requests on its own cache: the call, and what it has to give."""
+    r = np.random.default_rng(B)
+    lens, new = r.integers(0, 40, B), r.integers(0, 3, B)
+    need = int((-(-(lens + new) // P)).sum())
+    table = np.full((B, 4), -3)
+    ids, at = r.permutation(need + 5), 0
+    for b, n in enumerate(lens):
+        h = -(-int(n) // P)
+        table[b, :h] = ids[at:at + h]
+        at += h
+    free, rows = ids[at:], int(new.sum()) + 3
+    cache = PagedCache(1, 64, need + 5, P)
+    args = dev(lens), dev(new), dev(table), dev(free), dev([len(free)])
+    want = op.plan(lens, new, table, free, len(free), P, rows)
+
+    def check(p):
+        for got, w in zip((p.lens, p.cu, p.slots, p.positions, p.free_count, args[2]), want):
+            assert np.array_equal(got.cpu().numpy().reshape(np.shape(w)), w)
+        assert cache.check_device_error() == 0
+    return cache, args, rows, check
+
+
+@pytest.mark.parametrize("B", [3000, 4000, 8192])
+def test_plan_of_thousands_of_requests(B):
+    cache, args, rows, check = many_requests(B)
+    check(cache.plan(*args, rows=rows))
+
+
+def test_plans_of_unlike_sizes_from_two_threads():
+    """A kernel's shared memory is set for the device's context, whoever else is about to launch it."""
+    steps = [many_requests(B) for B in (3500, 8192)]
+    plans, errors = [None, None], []
+
+    def work(k):
+        cache, args, rows, _ = steps[k]
+        out = cache.new_plan(args[0].numel(), rows)
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.default_stream())
+        try:
+            for _ in range(2000):
+                plans[k] = cache.plan(*args, out=out, stream=s)
+        except Exception as e:                               # noqa: BLE001
+            errors.append(e)
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(2)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    torch.cuda.synchronize()
+    assert not errors
+    for (_, _, _, check), p in zip(steps, plans):
+        check(p)
