@@ -72,7 +72,20 @@ constexpr int kClusterBlocks = 16;     // blocks of keys of a clustered block at
 struct Way {
   enum { FEW, TILES, F32 } kind;
   int cells, cluster, entries, rows, tile, parts, least;
+  bool pack;                           // Q is copied to the scratch first
 };
+
+// The many-rows kernel reads Q through a tensor map, whose strides are not 0: an
+// expanded Q (rows or heads that stand on one another) is laid out in the scratch
+// for it, 16 bytes a thread and turn.
+__global__ void __launch_bounds__(256) pack_kernel(const Attend a, char* out, int vectors) {
+  const int64_t heads = (int64_t)a.H * a.G, total = a.rows * heads * vectors;
+  for (int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x; x < total; x += (int64_t)gridDim.x * 256) {
+    const int64_t th = x / vectors, t = th / heads, h = th - t * heads;
+    reinterpret_cast<uint4*>(out)[x] =
+        *reinterpret_cast<const uint4*>(a.Q + t * a.q_row_b + h * a.q_head_b + (x - th * vectors) * 16);
+  }
+}
 
 static Way way_of(const mp_paged_cache& c, const mp_paged_attend_args& p) {
   Way w{};
@@ -81,6 +94,7 @@ static Way way_of(const mp_paged_cache& c, const mp_paged_attend_args& p) {
   w.least = 1;
   if (c.cfg.dtype != MP_F32 && cells > kFewCells) {
     w.kind = Way::TILES;
+    w.pack = (p.rows > 1 && p.q_row_stride == 0) || (p.q_heads > 1 && p.q_head_stride == 0);
     w.rows = kTilesRows;
     w.tile = tiles_tokens(G);
     w.parts = c.sms;                   // one block an SM
@@ -108,8 +122,8 @@ static Way way_of(const mp_paged_cache& c, const mp_paged_attend_args& p) {
 
 static size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// The scratch of a split call: count, sums, entries, partial results.
-static size_t lay_work(const Way& w, int D, void* base, Work* out) {
+// The scratch of a split call: count, sums, entries, partial results, queries (16-bit, q_rows of head dim D).
+static size_t lay_work(const Way& w, int D, int64_t q_rows, void* base, Work* out, char** q) {
   if (w.entries == 0) return 0;
   size_t at = 256;
   const size_t before = at;
@@ -122,6 +136,8 @@ static size_t lay_work(const Way& w, int D, void* base, Work* out) {
   at = align256(at + (size_t)(w.parts + 1) * sizeof(int32_t));
   const size_t part = at;
   at = align256(at + (size_t)2 * w.parts * w.rows * (2 + D) * sizeof(float));
+  const size_t packed = at;
+  if (w.pack) at = align256(at + (size_t)q_rows * D * 2);
   if (out) {
     char* s = static_cast<char*>(base);
     out->count = reinterpret_cast<int32_t*>(s);
@@ -131,6 +147,7 @@ static size_t lay_work(const Way& w, int D, void* base, Work* out) {
     out->edge_entry = reinterpret_cast<int32_t*>(s + edge_entry);
     out->part = reinterpret_cast<float*>(s + part);
     out->parts = w.parts;
+    *q = s + packed;
   }
   return at;
 }
@@ -139,17 +156,28 @@ static size_t lay_work(const Way& w, int D, void* base, Work* out) {
 
 size_t paged_attend_scratch_bytes(const mp_paged_cache& c, const mp_paged_attend_args& p) {
   if (p.batch == 0 || p.rows == 0) return 0;
-  return paged::lay_work(paged::way_of(c, p), c.cfg.head_dim, nullptr, nullptr);
+  return paged::lay_work(paged::way_of(c, p), c.cfg.head_dim, (int64_t)p.rows * p.q_heads, nullptr, nullptr, nullptr);
 }
 
 mp_status paged_attend_impl(const mp_paged_cache& c, const mp_paged_attend_args& p, void* scratch, size_t,
                             cudaStream_t st) {
-  const paged::Attend a = paged::args_of(c, p);
+  paged::Attend a = paged::args_of(c, p);
   const paged::Way w = paged::way_of(c, p);
+  const int D = c.cfg.head_dim;
   cudaError_t e;
   paged::Work work{};
-  paged::lay_work(w, c.cfg.head_dim, scratch, &work);
+  char* q = nullptr;
+  paged::lay_work(w, D, (int64_t)p.rows * p.q_heads, scratch, &work, &q);
   work.least = w.least;
+  if (w.pack) {
+    const int vectors = D * 2 / 16;
+    const int64_t blocks = ((int64_t)p.rows * p.q_heads * vectors + 255) / 256;
+    paged::pack_kernel<<<(unsigned)std::min<int64_t>(blocks, (int64_t)c.sms * 8), 256, 0, st>>>(a, q, vectors);
+    if (cudaGetLastError() != cudaSuccess) return MP_ECUDA;
+    a.Q = q;
+    a.q_head_b = D * 2;
+    a.q_row_b = a.q_head_b * p.q_heads;
+  }
   if (w.kind == paged::Way::FEW) e = paged::attend_few(a, c, work, w.cells, w.cluster, st);
   else if (w.kind == paged::Way::TILES) e = paged::attend_tiles(a, c, work, st);
   else e = paged::attend_f32(a, c, work, w.rows, w.tile, w.cluster, st);

@@ -351,7 +351,7 @@ typedef struct {
   const int32_t* cu;                 /* [batch + 1] first row of each request */
   const void* Q;                     /* [rows, q_heads, head_dim] */
   void* O;                           /* the same; its rows overlap neither one another nor Q's */
-  int64_t q_row_stride, q_head_stride, o_row_stride, o_head_stride;  /* elements, 16-byte multiples */
+  int64_t q_row_stride, q_head_stride, o_row_stride, o_head_stride;  /* elements, 16-byte multiples; Q's may be 0 */
   float scale;                       /* 0: 1 / sqrt(head_dim) */
   float softcap;                     /* 0: none; else z = softcap * tanh(z / softcap) */
   int32_t window;                    /* 0: none; else a row sees the last `window` positions up to its own */

@@ -8,7 +8,7 @@ import torch
 from clustered_sparse_decode_b200 import Config, MpError, MultipoleIndex, PagedCache
 from clustered_sparse_decode_b200 import _lib as L
 from oracle import paged as op
-from paged_cases import TDT, Case, bounds, cache_of, call, dev
+from paged_cases import TDT, Case, bounds, cache_of, call, check, dev
 
 pytestmark = pytest.mark.gpu
 
@@ -195,3 +195,25 @@ def test_plans_of_unlike_sizes_from_two_threads():
     assert not errors
     for (_, _, _, check), p in zip(steps, plans):
         check(p)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("new", [1, 4, 60, 300])
+@pytest.mark.parametrize("axis", ["rows", "heads", "both"])
+def test_expanded_queries(dtype, new, axis):
+    """Queries whose rows or heads stand on one another, whichever kernel the number of rows leads to."""
+    c = Case([400, 333], [new, min(new, 333)], H=2, G=4, d=64, P=32, dtype=dtype, seed=19, poison=np.nan)
+    q = dev(c.Q, dtype)
+    q = q[:1] if axis != "heads" else q
+    q = (q[:, :1] if axis != "rows" else q).expand(c.rows, c.H * c.G, 64)
+    assert 0 in q.stride()
+    c.Q = q.double().cpu().numpy()
+    check(c, call(c, q=q), c.want())
+    cache, out = cache_of(c), torch.empty(c.rows, c.H * c.G, 64, dtype=TDT[dtype], device="cuda")
+    g = torch.cuda.CUDAGraph()
+    args = q, dev(c.table), dev(c.lens), dev(c.cu)
+    ref = cache.attend(*args, max_new=new)
+    with torch.cuda.graph(g):
+        cache.attend(*args, max_new=new, out=out)
+    g.replay()
+    assert torch.equal(out, ref) and cache.check_device_error() == 0
