@@ -31,7 +31,8 @@ class PagedCache:
     K, V: [num_pages, kv_heads, page_tokens, head_dim] on the device, allocated
     when absent.  Views with any order of the first three axes are taken as they
     are (equal strides for both, the last axis contiguous, 16-byte multiples),
-    so that a pool of another layout is passed as its permuted view.
+    so that a pool of another layout is passed as its permuted view.  The error
+    word is cleared on the current stream: calls on another one come after it.
     """
 
     def __init__(self, kv_heads, head_dim, num_pages, page_tokens, dtype="bf16", K=None, V=None, device=None):
@@ -46,7 +47,7 @@ class PagedCache:
         for t in (K, V):
             if tuple(t.shape) != want or t.dtype != self.torch_dtype or t.device.type != "cuda" or t.device != K.device:
                 raise ValueError(f"K and V must be {self.torch_dtype} device tensors of shape {want}")
-            if t.stride(3) != 1 or t.stride() != K.stride():
+            if t.stride(3) != 1 or any(n > 1 and a != b for n, a, b in zip(want, t.stride(), K.stride())):
                 raise ValueError("K and V need equal strides and contiguous rows")
         if device is not None and torch.device(device) not in (K.device, torch.device("cuda")):
             raise ValueError(f"K and V are on {K.device}")
@@ -58,7 +59,7 @@ class PagedCache:
         row = head_dim
         c.token_stride = K.stride(2) if page_tokens > 1 else row
         c.head_stride = K.stride(1) if kv_heads > 1 else max(row, K.stride(2) * page_tokens)
-        c.page_stride = K.stride(0) if num_pages > 1 else max(row, K.stride(2) * page_tokens, K.stride(1) * kv_heads)
+        c.page_stride = K.stride(0) if num_pages > 1 else max(row, K.stride(2) * page_tokens, c.head_stride * kv_heads)
         with torch.cuda.device(self.device):
             self._err = torch.zeros(1, dtype=torch.int32, device=self.device)
             self.h = L.MpPagedCache()
@@ -155,8 +156,8 @@ class PagedCache:
         shape = (T, self.kv_heads, self.head_dim)
         k, ks = self._rows(K_new, shape, "K_new")
         v, vs = self._rows(V_new, shape, "V_new")
-        if ks != vs:
-            raise ValueError("K_new and V_new need equal strides")
+        if ks != vs and ((T > 1 and ks[0] != vs[0]) or (self.kv_heads > 1 and ks[1] != vs[1])):
+            raise ValueError("K_new and V_new need equal strides")     # (an axis of length 1 has none that counts)
         self._run(stream, "mp_paged_append", self.lib.mp_paged_append, self._h, k, v, ks[0], ks[1],
                   self._ints(slots, T, "slots", torch.int64), T)
 

@@ -217,3 +217,38 @@ def test_expanded_queries(dtype, new, axis):
         cache.attend(*args, max_new=new, out=out)
     g.replay()
     assert torch.equal(out, ref) and cache.check_device_error() == 0
+
+
+def test_append_of_a_single_row_from_unlike_views():
+    """The strides of an axis of length 1 mean nothing, so K_new's and V_new's may differ there."""
+    cache = PagedCache(2, 64, 4, 16)
+    cache.K.zero_(), cache.V.zero_()
+    kv = torch.randn(1, 4, 64, device="cuda").bfloat16()
+    k, v = kv[:, :2], kv[:, 2:].clone(memory_format=torch.contiguous_format)
+    assert k.stride() != v.stride()
+    cache.append(k, v, torch.tensor([17], device="cuda"))
+    assert torch.equal(cache.K[1, :, 1], k[0]) and torch.equal(cache.V[1, :, 1], v[0])
+    one = PagedCache(1, 64, 4, 16)
+    x = torch.randn(3, 2, 64, device="cuda").bfloat16()
+    k, v = x[:, :1], x.transpose(0, 1).contiguous().transpose(0, 1)[:, 1:]
+    one.append(x[:, :1], x.as_strided((3, 1, 64), (128, 64, 1), 64), torch.tensor([1, 2, 3], device="cuda"))
+    one.append(k.as_strided((3, 1, 64), (128, 8, 1)), k, torch.tensor([5, 6, 7], device="cuda"))
+    assert torch.equal(one.K[0, 0, 5:8], k[:, 0]) and torch.equal(one.V[0, 0, 5:8], k[:, 0])
+
+
+def test_pool_of_a_single_page_or_head_from_unlike_views():
+    """The same for the pool's own K and V."""
+    kv = torch.zeros(2, 1, 3, 16, 64, dtype=torch.bfloat16, device="cuda")
+    K, V = kv[0], torch.zeros(1, 6, 16, 64, dtype=torch.bfloat16, device="cuda")[:, :3]
+    assert K.stride() != V.stride()
+    cache = PagedCache(3, 64, 1, 16, K=K, V=V)
+    x = torch.randn(2, 3, 64, device="cuda").bfloat16()
+    cache.append(x, x, torch.tensor([0, 15], device="cuda"))
+    for X in (K, V):
+        assert torch.equal(X[0, :, 0], x[0]) and torch.equal(X[0, :, 15], x[1])
+    one = torch.zeros(16 * 64, dtype=torch.bfloat16, device="cuda").as_strided((1, 1, 16, 64), (7, 12345, 64, 1))
+    cache = PagedCache(1, 64, 1, 16, K=one, V=torch.zeros_like(one))
+    cache.append(x[:, :1], x[:, :1], torch.tensor([0, 15], device="cuda"))
+    assert torch.equal(one[0, 0, 15], x[1, 0])
+    with pytest.raises(ValueError):
+        PagedCache(3, 64, 1, 16, K=K, V=torch.zeros(1, 16, 3, 64, dtype=torch.bfloat16, device="cuda").transpose(1, 2))
