@@ -167,13 +167,14 @@ class PagedCache:
 
         Request b's rows are cu[b] .. cu[b + 1] and hold its last tokens of the
         lens[b] that the cache has (append before attending).  A row sees the keys
-        up to its own position (all with full=True), those before prefix[b], only
-        the last `window` positions (0: all), and none before first_key[row].
-        Scores are scale * q.k, capped by softcap * tanh(z / softcap), minus
-        slopes[head] * |position - key|.  out must not overlap Q.  max_new: most rows that a request has (a
-        bound known to the host; it chooses the kernel).  Returns O [rows, Hq, d];
-        rows behind cu[B] are left as they are.  lse: float32 [rows, Hq] that
-        receives the log of each row's sum, -inf where it sees nothing.
+        up to its own position, or up to prefix[b] where that is further (all with
+        full=True); of these only the last `window` positions (0: all) and none
+        before first_key[row].  Scores are scale * q.k, capped by softcap *
+        tanh(z / softcap), minus slopes[head] * |position - key|.  max_new: most
+        rows that a request has (a bound known to the host; it chooses the
+        kernel).  Returns O [rows, Hq, d]; rows behind cu[B] are left as they are;
+        out must not overlap Q.  lse: float32 [rows, Hq] that receives the log of
+        each row's sum, -inf where it sees nothing.
         """
         if Q.dim() != 3:
             raise ValueError("Q must be [rows, heads, head_dim]")

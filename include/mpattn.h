@@ -296,7 +296,8 @@ const char* mp_decode_phases(const mp_index* idx);
  * and allocate nothing.  A data-dependent fault sets a bit of the cache's
  * error word and skips the access: 1 a page, slot, length or offset outside its
  * range, 4 a bounded wait gave up, 8 a step that does not fit (mp_paged_plan)
- * or a request with more rows than max_new (mp_paged_attend).
+ * or a request with more rows than max_new (mp_paged_attend).  What such a row or
+ * request gets has no meaning, but nothing of another request's pages.
  * ------------------------------------------------------------------------- */
 typedef struct {
   int32_t kv_heads, head_dim;        /* head_dim 64 or 128 */
@@ -357,7 +358,8 @@ typedef struct {
   int32_t window;                    /* 0: none; else a row sees the last `window` positions up to its own */
   uint32_t flags;                    /* MP_ATTEND_FULL */
   const float* slopes;               /* [q_heads] or NULL: z -= slopes[h] * |position - key|, after the cap */
-  const int32_t* prefix;             /* [batch] or NULL: every row also sees the keys before prefix[b] */
+  const int32_t* prefix;             /* [batch] or NULL: prefix[b] moves the end of a row's keys, not their beginning:
+                                      * up to it, a row also sees keys behind its own position */
   const int32_t* first_key;          /* [rows] or NULL: a row sees no key before first_key[row] */
   float* lse;                        /* [rows, q_heads] or NULL: log of the sum of exp(z); -inf for an empty row */
 } mp_paged_attend_args;
@@ -392,7 +394,8 @@ mp_status mp_paged_append(const mp_paged_cache* cache, const void* K_new, const 
  * position p (above) sees the keys j in [lo, hi), hi = max(p + 1, min(prefix,
  * len)) or len with MP_ATTEND_FULL, lo = max(first_key, p - window + 1);
  * z_j = scale q.k_j, capped, biased; O = sum e^z v / sum e^z over the keys it
- * sees, whatever other keys hold; 0 for a row that sees none.  Table entries of
+ * sees, whatever other keys hold (a column in which it sees infinities or NaN is
+ * that, however small their weights); 0 for a row that sees none.  Table entries of
  * pages before the first key that a request's rows see, and behind its len, are
  * not followed (a sliding window's pages may be given away).  Rows from
  * cu[batch] on are left as they were.  Accumulation and softmax are fp32.
