@@ -271,18 +271,20 @@ __device__ __forceinline__ float rcp(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// both forms and a selection: as a branch, rows' scores on both sides of 3/4 took twice the time
-__device__ __forceinline__ float cap_of(const Attend& a, float z) {
-  const float u = z * a.to_u, x = u * u;
-  float y = kTanh[5];
-#pragma unroll
-  for (int q = 4; q >= 0; --q) y = fmaf(y, x, kTanh[q]);
-  const float near = z * a.to_z * y, far = fmaf(-2.f * a.cap2, rcp(1.f + sc::ex2(u * (2.f * kLog2e))), a.cap2);
+// near's form for |u| <= 3/4, else far's: as a branch, rows with scores on both sides took twice the time
+__device__ __forceinline__ float select_near(float u, float near, float far) {
   float r;
   asm("{\n .reg .pred p;\n setp.le.f32 p, %1, %2;\n selp.f32 %0, %3, %4, p;\n}\n"
       : "=f"(r)
       : "f"(fabsf(u)), "f"(kTanhMost), "f"(near), "f"(far));
   return r;
+}
+__device__ __forceinline__ float cap_of(const Attend& a, float z) {
+  const float u = z * a.to_u, x = u * u;
+  float y = kTanh[5];
+#pragma unroll
+  for (int q = 4; q >= 0; --q) y = fmaf(y, x, kTanh[q]);
+  return select_near(u, z * a.to_z * y, fmaf(-2.f * a.cap2, rcp(1.f + sc::ex2(u * (2.f * kLog2e))), a.cap2));
 }
 
 // Weights that a product takes in the values' type are 2^(z - m + kLift): fp16's
