@@ -5,6 +5,7 @@
 #include <cmath>
 #include <cstring>
 #include <mutex>
+#include <utility>
 
 #include "paged_work.cuh"
 
@@ -497,12 +498,24 @@ static bool rows_meet(int64_t shift, int64_t rows, int64_t heads, int64_t row, i
   if (heads == 1) head = 0;
   if (shift == 0 && (row >= (wide)(heads - 1) * head + d || rows == 1) && (head >= d || heads == 1)) return false;
   if (shift == 0 && (head >= (wide)(rows - 1) * row + d || heads == 1) && (row >= d || rows == 1)) return false;
-  for (int64_t j = 1 - heads; j < heads; ++j) {
-    const wide at = (wide)shift + (wide)j * head;
-    const wide near = row > 0 ? -at / row : 0;           // the i that brings the two rows nearest, or its neighbour
-    for (wide i = near - 1; i <= near + 1; ++i) {
-      if (i <= -rows || i >= rows || (shift == 0 && i == 0 && j == 0)) continue;
-      const wide apart = at + i * row;
+  // where one axis steps over all of the other, few pairs can be near; otherwise the shorter is gone through
+  const bool over = row >= (wide)(heads - 1) * head + d, under = head >= (wide)(rows - 1) * row + d;
+  if (!over && (under || heads < rows)) {
+    std::swap(rows, heads);
+    std::swap(row, head);
+  }
+  int64_t i0 = 1 - rows, i1 = rows;
+  if (over || under) {
+    const wide q = -(wide)shift / row;
+    i0 = (int64_t)std::max<wide>(i0, q - 1);
+    i1 = (int64_t)std::min<wide>(i1, q + 2);
+  }
+  for (int64_t i = i0; i < i1; ++i) {
+    const wide at = (wide)shift + (wide)i * row;
+    const wide near = head > 0 ? -at / head : 0;         // the j that brings the two rows nearest, or its neighbour
+    for (wide j = near - 1; j <= near + 1; ++j) {
+      if (j <= -heads || j >= heads || (shift == 0 && i == 0 && j == 0)) continue;
+      const wide apart = at + j * head;
       if (apart < d && apart > -d) return true;
     }
   }
