@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Attend a, c
       float f = 0.f;
       if (i0 + k < np && row < cells) {
         const float mi = slot(i0 + k)[row];
-        f = mi == -INFINITY ? 0.f : exp2f(mi - m);
+        f = part_factor(mi, m);
         l = fmaf(f, slot(i0 + k)[rows + row], l);
       }
       for (int k0 = 0; k0 < min(K, np - i0); k0 += S) {

@@ -115,6 +115,12 @@ template <int ROWS>
 struct Again {
   int bad[ROWS], low, high;
 };
+// The factor of a part with maximum mp where all have m: never 0 for a part that saw
+// keys, so that its infinities and NaN stay (of finite numerators less than 2^-21 is
+// left then).
+__device__ __forceinline__ float part_factor(float mp, float m) {
+  return mp == -INFINITY ? 0.f : fmaxf(exp2f(mp - m), 0x1p-149f);
+}
 template <typename T>
 __device__ __forceinline__ void settle_final(const Attend& a, const Settle& s, int row, int c, float m, float l, float v) {
   const bool none = l == 0.f;
@@ -230,7 +236,7 @@ __device__ void settle(const Attend& a, const Settle& s, const float* ml, float*
     float m = -INFINITY, l = 0.f, v = 0.f;
     for (int p = 0; p < s.cluster; ++p) m = fmaxf(m, cl.map_shared_rank(unit, p)[row]);
     for (int p = 0; p < s.cluster; ++p) {
-      const float mp = cl.map_shared_rank(unit, p)[row], k = mp == -INFINITY ? 0.f : exp2f(mp - m);
+      const float mp = cl.map_shared_rank(unit, p)[row], k = part_factor(mp, m);
       l = fmaf(k, cl.map_shared_rank(unit, p)[ROWS + row], l);
       if (k != 0.f) v = fmaf(k, cl.map_shared_rank(num, p)[row * PITCH + c], v);
     }

@@ -37,7 +37,7 @@ def test_bad_values_of_one_request_stay_its_own(dtype, d, new, kind, qscale):
     """An early NaN and a late infinity among one long request's values: in its own rows where they belong, in the
     columns that hold them, and nowhere else, however small their weights; other requests' rows are written as without
     it."""
-    c = Case([16400, 16400, 700], [new] * 3, H=1, G=4, d=d, P=64, dtype=dtype, seed=31, qscale=qscale)
+    c = Case([16400, 700], [new] * 2, H=1, G=4, d=d, P=64, dtype=dtype, seed=31, qscale=qscale)
     want = c.want()
     tol, ltol = bounds(c, want[2], want[0], want[1])
     late = 16400 - min(50, new // 2 + 1)
@@ -252,3 +252,27 @@ def test_pool_of_a_single_page_or_head_from_unlike_views():
     assert torch.equal(one[0, 0, 15], x[1, 0])
     with pytest.raises(ValueError):
         PagedCache(3, 64, 1, 16, K=K, V=torch.zeros(1, 16, 3, 64, dtype=torch.bfloat16, device="cuda").transpose(1, 2))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("G,new", [(1, 1), (8, 4), (1, 64)])
+@pytest.mark.parametrize("n", [600, 30000])
+def test_infinities_and_nan_outlast_any_factor(dtype, G, new, n):
+    """Keys whose weights beside the others' underflow, in a part of the keys that others finish: what is not finite among
+    them is still seen, what is finite has no weight."""
+    c = Case([n], [new], H=1, G=G, d=64, P=32, dtype=dtype, seed=23)
+    page, row = c.at(0, np.arange(n))
+    c.Q[:], c.K[:] = 0.0, 0.0
+    c.Q[:, :, 0] = 1.0
+    c.K[page, 0, row, 0] = np.where(np.arange(n) < n // 2, -1000.0, 0.0)
+    want = c.want(scale=1.0)
+    tol = bounds(c, want[2], want[0], want[1])[0]
+    O = want[0].copy()
+    for j, col, bad in ((3, 7, np.inf), (40, 9, np.nan), (n // 2 - 300, 11, -np.inf), (3, 13, np.inf), (n // 2 - 1, 13, -np.inf)):
+        page, row = c.at(0, j)
+        c.V[page, 0, row, col] = bad
+        O[..., col] = np.nan if np.isinf(O[0, 0, col]) else bad
+    got = call(c, scale=1.0)[0]
+    odd = ~np.isfinite(O)
+    assert np.array_equal(got[odd], O[odd], equal_nan=True)
+    assert (np.abs(got[~odd] - O[~odd]) <= tol[~odd]).all()
