@@ -9,8 +9,9 @@
 // wait for each other until the share ends).  Two blocks lie on an SM, 12
 // stages of 8 KB (head dim 128) each: 192 KB in flight, and one block's ends of
 // shares fall into the other's stream.  Measured: 16 requests of 16K to 32K tokens
-// (32 query heads on 8 of 128, bf16, pages of 16) 277 us, 6.2 TB/s, 94% of a copy's
-// rate; one of 64K, fp16, 62 us, 4.3 TB/s: 41 us of bytes, the rest the blocks' first
+// (32 query heads on 8 of 128, bf16, pages of 16) 277 to 283 us, 6.0 to 6.2 TB/s, 92
+// to 94% of a copy's rate; drafts of 8 tokens on them (32 rows a KV head) 307 us; one
+// request of 64K, fp16, 62 us, 4.3 TB/s: 41 us of bytes, the rest the blocks' first
 // loads (lengths, table, keys, one after the other) and the joining of 37 parts.
 //
 // Rows are the M of mma.sync m16n8k16 (S = Q K^T with 16 keys as N, O += P V

@@ -15,22 +15,23 @@
 // S, the tensor cores do the other half's two products.  They need 2 x 512
 // cycles a half and block at head dim 128, the exponentials 1024 a half: both
 // units are the bound, about equally.  Measured, 4K bf16 tokens over 12K (32 query
-// heads on 8 of 128): 0.72 to 0.77 ms in a single call, 1.25 to 1.33 PFLOP/s, the
-// tensor cores busy 65% of the cycles; 0.89 ms (1.08 PFLOP/s) one call after the
-// other, when the card's power limit lowers the clock.  What is left is the chain of
-// a half's block, whose parts cannot overlap for want of tensor memory: S is ready,
-// softmax (1900 cycles of one warp a scheduler), the rest of P V and the next S.
+// heads on 8 of 128): 0.82 ms in a single call, list and joining included, 0.79 ms
+// (1.22 PFLOP/s) this kernel's launch alone, the tensor cores busy 64% of the
+// cycles; 0.80 to 0.90 ms one call after the other, as the card's power limit lowers
+// the clock.  What is left is the chain of a half's block, whose parts cannot overlap
+// for want of tensor memory: S is ready, softmax (1900 cycles of one warp a
+// scheduler), the rest of P V and the next S.
 //
 // The running maximum is lazy (it moves when a score exceeds it by more than 8
 // in base 2), so that O is rarely read back and rescaled; the sums use the
 // weights before they are rounded to the values' type for the second product.
 // That rounding, at most half a step a weight, is what the tensor cores' operand
-// costs: a remainder as a second operand would make P V twice as long.  Against 64
-// bits the 4K tokens above are off by 2.4e-3 at most, 1.65e-3 with fp32 weights.
-// Keys that a row does not see have weight exactly 0; values behind a request's
-// last token are zeroed in shared memory, and a row whose result is not finite
-// is done again key by key, since a value that it does not see may have been
-// infinite or NaN.
+// costs: a remainder as a second operand would make P V twice as long.  The error
+// against 64 bits is 1.4 times that of fp32 weights (4K tokens above: 2.3e-3 and
+// 1.7e-3 of the outputs, most of it the outputs' own rounding to bf16).  Keys that a
+// row does not see have weight exactly 0; values behind a request's last token are
+// zeroed in shared memory, and a row whose result is not finite is looked at again
+// (mend_rows), since a value that it does not see may have been infinite or NaN.
 #include <cudaTypedefs.h>
 
 #include <cstring>
@@ -590,7 +591,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
           for (int q = 0; q < 16; ++q) {
             const float2 x = fma2(make_float2(z[2 * q], z[2 * q + 1]), mul, sub);
             // every fourth pair by arithmetic: the exponential unit alone needs 1024 cycles a half, as long as the
-            // products (none: 745 us for 4K tokens over 12K, two of eight in a row 731, every fourth 721, three 745)
+            // products (none: 846 us for 4K tokens over 12K in a single call, every eighth 837, fourth 817, third 950)
             const float2 w = (q & 3) == 3 ? exp2_pair(x) : make_float2(sc::ex2(x.x), sc::ex2(x.y));
             sum[q & 1] = add2(sum[q & 1], w);
             p[q] = to_pair<T>(w.x, w.y);
