@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) few_kernel(const __grid_con
       for (int s = 0; s < 2; ++s) {
         const int row = DUP ? g : mt * 16 + s * 8 + g;
         if (row >= cells) {
-          if (t4 == 0) mine[row] = make_int4(0, INT32_MAX, 0, 0);
+          if (t4 == 0) mine[row] = make_int4(0, 0, 0, 0);
           continue;
         }
         const Interval v = interval_of(a, r, prefix, row / a.G);

@@ -548,6 +548,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
         tc_after();
         const int kb = it.key0 + j * kKeys, lo = v.lo - kb, hi = v.hi - kb;
         const bool cut = __any_sync(kFull, v.lo > kb || v.hi < kb + kKeys);
+        const float say = valid ? INFINITY : 0.f;
         // which of the 32 columns from 32 k on this row sees
         auto seen = [&](int k) {
           const int from = min(max(lo - 32 * k, 0), 32), to = min(max(hi - 32 * k, 0), 32);
@@ -566,9 +567,10 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
           sc::fence_proxy_async();
           return true;
         };
-        // the running maximum, in base 2, and with it the numerator, whose last product has ended with this S
+        // the running maximum, in base 2, and with it the numerator, whose last product has ended with this S (a warp's
+        // rows together: those that are none, whose scores come of anything, have no say)
         auto raise = [&](float mx) {
-          if (!__any_sync(kFull, mx > m + 8.f)) return;
+          if (!__any_sync(kFull, valid && mx > m + 8.f)) return;
           const float nm = fmaxf(m, mx), keep = m == -INFINITY ? 0.f : sc::ex2(m - nm);
           m = nm;
           l *= keep;
@@ -640,11 +642,18 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
             tmem_ld_wait(z);
             if (a.cap > 0.f) {
               // the exponential (two results of a unit that the weights need too) only where some |u| of the warp's 32
-              // columns is above 3/4
+              // columns is above 3/4; what memory happened to hold behind the last token has no say, nor has a row that is none
+              const int held = it.r.len - kb - 32 * k;
+              if (held < 32) {
+#pragma unroll
+                for (int q = 0; q < 32; ++q)
+                  if (q >= held) z[q] = 0.f;
+              }
               float t[4] = {};
 #pragma unroll
               for (int q = 0; q < 32; q += 2) t[q / 2 & 3] = max3(t[q / 2 & 3], fabsf(z[q]), fabsf(z[q + 1]));
-              const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), far = top <= 0x1p60f ? top * fabsf(a.to_u) : 1.f;
+              const float top = fminf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), say),
+                          far = top <= 0x1p60f ? top * fabsf(a.to_u) : 1.f;
               if (__all_sync(kFull, far <= fminf(most, 0.3125f))) {
 #pragma unroll
                 for (int q = 0; q < 32; q += 2) {

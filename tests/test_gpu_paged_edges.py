@@ -276,3 +276,26 @@ def test_infinities_and_nan_outlast_any_factor(dtype, G, new, n):
     odd = ~np.isfinite(O)
     assert np.array_equal(got[odd], O[odd], equal_nan=True)
     assert (np.abs(got[~odd] - O[~odd]) <= tol[~odd]).all()
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("f16", 64), ("f32", 64)])
+@pytest.mark.parametrize("new", [1, 3, 60, 300])
+@pytest.mark.parametrize("kw", [{}, dict(softcap=2.0), dict(window=90)], ids=["plain", "cap", "window"])
+def test_results_are_the_same_bits_after_other_calls(dtype, d, new, kw):
+    """What earlier calls leave in an SM's memories, and what lies behind a request's tokens, moves no bit of the result."""
+    c = Case([400, 333, 70], [new, new, min(new, 70)], H=2, G=4, d=d, P=32, dtype=dtype, seed=19, poison=0.0)
+    first = call(c, **kw)
+    others = []
+    for k, fill in enumerate((np.nan, 30.0, -50.0)):
+        o = Case([900, 500], [61, 300], H=2, G=4, d=d, P=32, dtype=dtype, seed=50 + k, poison=fill, qscale=10.0 ** k)
+        o.K *= 5.0
+        others.append((o, cache_of(o)))
+    caches = [cache_of(c)]
+    for fill in (np.nan, 100.0):
+        x = Case(c.lens, c.new, H=2, G=4, d=d, P=32, dtype=dtype, seed=19, poison=fill)
+        caches.append(cache_of(x))
+    for turn in range(30):
+        o, cache = others[turn % 3]
+        cache.attend(dev(o.Q, dtype), dev(o.table), dev(o.lens), dev(o.cu), max_new=300)
+        got = call(c, cache=caches[turn % len(caches)], **kw)
+        assert np.array_equal(got[0], first[0]) and np.array_equal(got[1], first[1]), turn
