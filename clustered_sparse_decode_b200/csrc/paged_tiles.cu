@@ -433,12 +433,14 @@ __device__ __forceinline__ uint32_t to_pair(float lo, float hi) {
   }
 }
 
-// GEN: scores are capped or biased, or the scale is negative: the exponent is
-// formed first, and its factor is 1.
-template <typename T, int D, bool GEN>
+// CAP, BIAS: scores are capped, biased (or the scale is negative): the exponent is
+// formed first, and its factor is 1.  A kernel for each, as their loops have to
+// stay in the instruction cache.
+template <typename T, int D, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_constant__ Tiles f) {
   using C = TilesCfg<D>;
   constexpr int NS = C::NS, KT = C::KT;
+  constexpr bool GEN = CAP || BIAS;
   const Attend& a = f.a;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (sc::smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -541,7 +543,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
       const bool valid = i < it.r.n;
       Interval v{0, INT32_MAX, 0};
       if (valid) v = interval_of(a, it.r, prefix_of(a, it.b), i);
-      const float slope = GEN && a.slopes ? __ldg(a.slopes + hq) * kLog2e : 0.f;
+      const float slope = BIAS && a.slopes ? __ldg(a.slopes + hq) * kLog2e : 0.f;
       float m = -INFINITY, l = 0.f;
       for (int j = it.from[g]; j < it.to[g]; ++j) {
         if (!wait(s_full + 8 * g, n_s++ & 1u)) break;
@@ -640,7 +642,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
             float z[32];
             tmem_ld(tS + 32 * k, z);
             tmem_ld_wait(z);
-            if (a.cap > 0.f) {
+            if constexpr (CAP) {
               // the exponential (two results of a unit that the weights need too) only where some |u| of the warp's 32
               // columns is above 3/4; what memory happened to hold behind the last token has no say, nor has a row that is none
               const int held = it.r.len - kb - 32 * k;
@@ -693,7 +695,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
                 z[q + 1] = y.y;
               }
             }
-            if (a.slopes) {
+            if (BIAS && a.slopes) {
               const float d = ahead - (float)(32 * k);
               if (__all_sync(kFull, straight || d >= 31.f)) {    // no key behind a row, or none that it sees
                 const float2 at = make_float2(-slope * d, -slope * d), by = make_float2(slope, slope);
@@ -961,10 +963,10 @@ __global__ void __launch_bounds__(kTilesThreads, 1) tiles_kernel(const __grid_co
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
-template <typename T, int D, bool GEN>
+template <typename T, int D, bool CAP, bool BIAS>
 static cudaError_t launch_tiles_t(const Tiles& f, cudaStream_t st) {
   using C = TilesCfg<D>;
-  auto kern = tiles_kernel<T, D, GEN>;
+  auto kern = tiles_kernel<T, D, CAP, BIAS>;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)f.w.parts);
   cfg.blockDim = dim3(kTilesThreads);
@@ -981,8 +983,8 @@ static cudaError_t launch_tiles_t(const Tiles& f, cudaStream_t st) {
 
 template <typename T, int D>
 static cudaError_t launch_tiles(const Tiles& f, cudaStream_t st) {
-  const bool gen = f.a.cap > 0.f || f.a.slopes || f.a.scale < 0.f;
-  return gen ? launch_tiles_t<T, D, true>(f, st) : launch_tiles_t<T, D, false>(f, st);
+  if (f.a.cap > 0.f) return f.a.slopes ? launch_tiles_t<T, D, true, true>(f, st) : launch_tiles_t<T, D, true, false>(f, st);
+  return f.a.slopes || f.a.scale < 0.f ? launch_tiles_t<T, D, false, true>(f, st) : launch_tiles_t<T, D, false, false>(f, st);
 }
 
 // Q as [row][head][d]: a box is one KV head's query heads of kHalf / G rows, 64
